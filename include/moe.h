@@ -248,6 +248,17 @@ moe_status moe_permute_mxfp8(const moe_shape* shape, const void* x, const int32_
                              int32_t* slot_pos, void* x_perm_q, void* x_perm_sf, void* ws,
                              size_t ws_bytes, void* stream);
 
+/* moe_permute_mxfp8 for tokens that are held in MXFP8 already (y_q and y_sf of
+ * moe_rmsnorm): x_q [T, d] E4M3 bytes, x_sf [T, d/32] scale bytes.  Every routed
+ * row receives its token's codes and scales unchanged; the layout outputs and
+ * the errors are those of moe_permute_mxfp8.  Rows >= offsets[N] of x_perm_q and
+ * x_perm_sf are not written. */
+moe_status moe_permute_mxfp8_rows(const moe_shape* shape, const void* x_q, const void* x_sf,
+                                  const int32_t* topk_idx, const int32_t* counts,
+                                  int32_t* offsets, int32_t* row_token, int32_t* slot_pos,
+                                  void* x_perm_q, void* x_perm_sf, void* ws, size_t ws_bytes,
+                                  void* stream);
+
 /* h = SiLU(x_perm W1_e^T) * (x_perm W3_e^T) on MXFP8 operands (fp32
  * accumulation), written as MXFP8: h_q [T*K, I] bytes, h_sf [T*K, I/32]. */
 moe_status moe_expert_gate_up_mxfp8(const moe_shape* shape, const void* x_perm_q,
@@ -260,6 +271,50 @@ moe_status moe_expert_gate_up_mxfp8(const moe_shape* shape, const void* x_perm_q
 moe_status moe_expert_down_mxfp8(const moe_shape* shape, const void* h_q, const void* h_sf,
                                  const void* w2_q, const void* w2_sf, const int32_t* offsets,
                                  void* y_perm, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- 4-bit expert path ---------------------------------------------------
+ * Experts with 4-bit weights and group scales for decode batches; the
+ * activations keep the layer's dtype and sums are fp32:
+ *   W[n, k] = (code[n, k] - 8) * scale[n, k / group],  code in 0..15,
+ *   group 32, 64 or 128 columns along the contraction axis, scales bf16.
+ * Any number of rows and columns: blocks of 16 rows x 128 columns, ordered
+ * (matrix, row block, column block), the edge blocks padded with zero weights.
+ * One block is 1024 bytes of codes, 64 a row; bytes 16 t + 4 j .. + 3 of a row
+ * are a little-endian word with columns 32 j + 8 t .. + 7 of the block, nibble p
+ * of it column 2 p (p < 4) or 2 (p - 4) + 1 of those eight.  Scales:
+ * [matrix, row block, column block, 16, 128 / group].  The shape's weight_layout
+ * is ignored.  Row lengths d and I must be multiples of 16 bytes (8 bf16 or 4
+ * fp32 values). */
+
+/* Bytes of the codes and of the scales of n_mats matrices [rows, cols] (0 for
+ * invalid arguments). */
+size_t moe_w4_code_bytes(int32_t n_mats, int32_t rows, int32_t cols);
+size_t moe_w4_scale_bytes(int32_t n_mats, int32_t rows, int32_t cols, int32_t group);
+
+/* Quantises n_mats row-major matrices [rows, cols] of `dtype` (contraction axis
+ * = cols; w1/w3 as N matrices [I, d], w2 as N matrices [d, I]):
+ * scale = amax / 7 over the group, rounded to bf16; code = 8 + w / scale rounded
+ * to nearest even (8 where the scale is 0).  Weights must be finite.  Done once
+ * when the weights are loaded. */
+moe_status moe_quantize_weights_w4(int32_t n_mats, int32_t rows, int32_t cols, int32_t group,
+                                   int32_t dtype, const void* src, void* dst_q, void* dst_s,
+                                   void* stream);
+
+/* moe_expert_gate_up_gather on 4-bit weights:
+ *   h[r, :] = SiLU(x[row_token[r], :] W1_e^T) * (x[row_token[r], :] W3_e^T).
+ * row_token NULL: the rows are read in place, x is x_perm [T*K, d].  A row_token
+ * entry outside [0, T) sets MOE_DEV_BAD_OFFSETS and reads row 0.  h [T*K, I];
+ * rows >= offsets[N] are not written. */
+moe_status moe_expert_gate_up_w4(const moe_shape* shape, int32_t group, const void* x,
+                                 const int32_t* row_token, const void* w1_q, const void* w1_s,
+                                 const void* w3_q, const void* w3_s, const int32_t* offsets,
+                                 void* h, void* ws, size_t ws_bytes, void* stream);
+
+/* y_perm[r, :] = h[r, :] W2_e^T on 4-bit weights.  Rows >= offsets[N] are not
+ * written. */
+moe_status moe_expert_down_w4(const moe_shape* shape, int32_t group, const void* h,
+                              const void* w2_q, const void* w2_s, const int32_t* offsets,
+                              void* y_perm, void* ws, size_t ws_bytes, void* stream);
 
 /* Weighted sum of Eq. (1) with the zero-computation experts folded in:
  *   out[t, :] = gamma * ( sum_{k: idx < N} gate[t,k] * y_perm[slot_pos[t,k], :]
@@ -390,6 +445,70 @@ moe_status moe_permute_backward(const moe_shape* shape, const void* dout,
                                 const int32_t* topk_idx, const float* topk_gate,
                                 const int32_t* slot_pos, const void* dx_perm,
                                 const float* dx_router, float gamma, void* dx, void* stream);
+
+/* ---- Residual RMS norm in front of the layer -----------------------------
+ *   s = x + residual, rounded to the dtype     (s = x when residual is NULL)
+ *   inv_rms[t] = 1 / sqrt(mean_j s[t, j]^2 + eps)                    (fp32)
+ *   y[t, j] = s[t, j] * inv_rms[t] * weight[j], rounded once
+ * x, residual, sum_out, y [T, d] and weight [d] have the dtype.  sum_out receives
+ * s and is required with a residual, NULL without one.  inv_rms [T] fp32 or NULL
+ * (the backward pass needs it).  y_q [T, d] and y_sf [T, d/32] (both or neither):
+ * y in MXFP8 (the format of the MXFP8 expert path, row-major), quantised from the
+ * rounded y so that it equals a later quantisation of it; bf16 only, d % 32 == 0.
+ * y may be NULL when y_q is given.  sum_out may be x or residual, and y may be x
+ * when there is no residual.  y in 8 bits must be finite.
+ * d must be a multiple of 16 bytes; eps finite and >= 0.  With T == 0 nothing is
+ * launched. */
+moe_status moe_rmsnorm(int32_t T, int32_t d, int32_t dtype, const void* x, const void* residual,
+                       const void* weight, float eps, void* sum_out, void* y, float* inv_rms,
+                       void* y_q, void* y_sf, void* stream);
+
+/* Bytes of device workspace moe_rmsnorm_backward needs (fp32 partial weight
+ * gradients).  Returns 0 for invalid arguments. */
+size_t moe_rmsnorm_workspace_bytes(int32_t T, int32_t d);
+
+/* Backward of moe_rmsnorm, for dy = dL/dy and dsum = dL/ds, the gradient that
+ * reaches s along the residual stream (NULL: none).  xhat = s * inv_rms:
+ *   dx = inv_rms * (weight * dy - xhat * mean_j(weight * dy * xhat)) + dsum
+ *   dweight[j] = sum_t dy[t, j] * xhat[t, j]
+ * dx is the gradient of x and of residual.  s is sum_out of the forward call (x
+ * without a residual), inv_rms its output.  Sums are fp32 in a fixed order; dx
+ * [T, d] and dweight [d] have the dtype and are rounded once.  dx may be dy or
+ * dsum.  With T == 0 dweight is set to zero. */
+moe_status moe_rmsnorm_backward(int32_t T, int32_t d, int32_t dtype, const void* s,
+                                const void* weight, const float* inv_rms, const void* dy,
+                                const void* dsum, void* dx, void* dweight, void* ws,
+                                size_t ws_bytes, void* stream);
+
+/* ---- Global gradient norm and clipping -----------------------------------
+ * One tensor of a gradient list: numel contiguous elements of dtype at grad;
+ * moe_grad_clip writes them to out (out == grad: in place).  The list itself is
+ * a HOST array, read before the call returns.  Tensors need the alignment of
+ * their elements only; empty ones are skipped.  The outs may overlap neither
+ * one another nor another tensor's grad. */
+typedef struct {
+  const void* grad;
+  void* out;
+  int64_t numel;
+  int32_t dtype; /* moe_dtype */
+} moe_grad;
+
+/* Bytes of device workspace for a list of n_tensors (0 for a negative n).  Clear
+ * it once with moe_workspace_init. */
+size_t moe_grad_workspace_bytes(int32_t n_tensors);
+
+/* *norm = sqrt(sum of g^2 over every element of every tensor), fp32 on the
+ * device; 0 for an empty list.  Squares are formed in fp32 (entries above 1.8e19
+ * in magnitude make the norm infinite) and summed in fp64, in a fixed order. */
+moe_status moe_grad_norm(int32_t n_tensors, const moe_grad* list, float* norm, void* ws,
+                         size_t ws_bytes, void* stream);
+
+/* out = grad * min(1, max_norm / (*norm + 1e-6)), rounded once; norm is a device
+ * pointer (of moe_grad_norm, or a norm joined over ranks).  A NaN norm makes every
+ * element NaN; an infinite one makes finite elements 0.  When the factor is 1 and
+ * every tensor is clipped in place, nothing is written. */
+moe_status moe_grad_clip(int32_t n_tensors, const moe_grad* list, float max_norm,
+                         const float* norm, void* stream);
 
 /* Synchronises `stream`, reads the workspace status word into *status_out
  * (may be NULL) and clears it.  Returns MOE_ERR_DEVICE_STATUS when it was

@@ -41,6 +41,23 @@ SIGNATURES = {
     "moe_expert_gate_up_mxfp8": (ctypes.c_int, [_SP, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                                 _vp, _sz, _vp]),
     "moe_expert_down_mxfp8": (ctypes.c_int, [_SP, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "moe_permute_mxfp8_rows": (ctypes.c_int, [_SP, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                              _vp, _sz, _vp]),
+    "moe_w4_code_bytes": (_sz, [_i32, _i32, _i32]),
+    "moe_w4_scale_bytes": (_sz, [_i32, _i32, _i32, _i32]),
+    "moe_quantize_weights_w4": (ctypes.c_int, [_i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp,
+                                               _vp]),
+    "moe_expert_gate_up_w4": (ctypes.c_int, [_SP, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                             _vp, _sz, _vp]),
+    "moe_expert_down_w4": (ctypes.c_int, [_SP, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "moe_rmsnorm": (ctypes.c_int, [_i32, _i32, _i32, _vp, _vp, _vp, _f32, _vp, _vp, _vp, _vp,
+                                   _vp, _vp]),
+    "moe_rmsnorm_workspace_bytes": (_sz, [_i32, _i32]),
+    "moe_rmsnorm_backward": (ctypes.c_int, [_i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                            _vp, _sz, _vp]),
+    "moe_grad_workspace_bytes": (_sz, [_i32]),
+    "moe_grad_norm": (ctypes.c_int, [_i32, _vp, _vp, _vp, _sz, _vp]),
+    "moe_grad_clip": (ctypes.c_int, [_i32, _vp, _f32, _vp, _vp]),
     "moe_workspace_bytes": (_sz, [_SP]),
     "moe_workspace_init": (ctypes.c_int, [_vp, _sz, _vp]),
     "moe_route": (ctypes.c_int,
@@ -142,6 +159,36 @@ def _p(t, dtype=None, name="tensor"):
     return ctypes.c_void_p(t.data_ptr())
 
 
+_DTYPE_CODES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+
+
+def _here(*tensors):
+    """The tensors lie on the current device, where the call launches."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.is_cuda and t.get_device() != dev:
+            raise ValueError(f"tensor on cuda:{t.get_device()}, but the current device is "
+                             f"cuda:{dev}")
+
+
+def _rows(x):
+    if x.dim() != 2 or x.dtype not in _DTYPE_CODES:
+        raise ValueError(f"rows must be a 2-d float32 or bfloat16 tensor, not {x.dtype} "
+                         f"{tuple(x.shape)}")
+    return x.shape[0], x.shape[1], _DTYPE_CODES[x.dtype]
+
+
+def _same(x, named):
+    for name, t in named:
+        if t is not None and t.shape != x.shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(x.shape)}")
+
+
+def _size(t, n, name):
+    if t is not None and t.numel() != n:
+        raise ValueError(f"{name} has {t.numel()} elements, expected {n}")
+
+
 def _stream(stream=None):
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
@@ -204,19 +251,276 @@ class Mxfp8Buffers:
 
 
 def forward_mxfp8(buf: "LayerBuffers", fb: Mxfp8Buffers, x, w_router, w1, w3, w2, bias,
-                  gamma=1.0, logit_offset=None, stream=None):
-    """The layer with MXFP8 experts: w1, w3, w2 are (codes, scales) pairs."""
+                  gamma=1.0, logit_offset=None, stream=None, x_q=None):
+    """The layer with MXFP8 experts: w1, w3, w2 are (codes, scales) pairs.  x_q: x in
+    MXFP8 too (the codes and scales of rmsnorm), so that the dispatch copies them
+    instead of quantising x again."""
     s = buf.shape
     route(s, x, w_router, bias, buf.ws, buf.topk_idx, buf.topk_gate, buf.counts, buf.n_ffn,
           logit_offset=logit_offset, probs_out=buf.probs, stream=stream)
-    permute_mxfp8(s, x, buf.topk_idx, buf.counts, buf.offsets, buf.row_token, buf.slot_pos,
-                  fb.x_perm_q, fb.x_perm_sf, buf.ws, stream=stream)
+    if x_q is not None:
+        permute_mxfp8_rows(s, x_q[0], x_q[1], buf.topk_idx, buf.counts, buf.offsets,
+                           buf.row_token, buf.slot_pos, fb.x_perm_q, fb.x_perm_sf, buf.ws,
+                           stream=stream)
+    else:
+        permute_mxfp8(s, x, buf.topk_idx, buf.counts, buf.offsets, buf.row_token, buf.slot_pos,
+                      fb.x_perm_q, fb.x_perm_sf, buf.ws, stream=stream)
     expert_gate_up_mxfp8(s, fb.x_perm_q, fb.x_perm_sf, w1, w3, buf.offsets, fb.h_q, fb.h_sf,
                          buf.ws, stream=stream)
     expert_down_mxfp8(s, fb.h_q, fb.h_sf, w2, buf.offsets, buf.y_perm, buf.ws, stream=stream)
     combine(s, x, buf.y_perm, buf.topk_idx, buf.topk_gate, buf.slot_pos, gamma, buf.out,
             stream=stream)
     return buf.out
+
+
+def permute_mxfp8_rows(shape, x_q, x_sf, topk_idx, counts, offsets, row_token, slot_pos, x_perm_q,
+                       x_perm_sf, ws, stream=None):
+    """permute_mxfp8 for tokens held in MXFP8 already (rmsnorm's y_q, y_sf)."""
+    _here(x_q, x_sf, x_perm_q, x_perm_sf, ws)
+    _check(lib().moe_permute_mxfp8_rows(ctypes.byref(shape), _p(x_q, torch.uint8, "x_q"),
+                                        _p(x_sf, torch.uint8, "x_sf"),
+                                        _p(topk_idx, torch.int32, "topk_idx"),
+                                        _p(counts, torch.int32, "counts"),
+                                        _p(offsets, torch.int32, "offsets"),
+                                        _p(row_token, torch.int32, "row_token"),
+                                        _p(slot_pos, torch.int32, "slot_pos"),
+                                        _p(x_perm_q, torch.uint8, "x_perm_q"),
+                                        _p(x_perm_sf, torch.uint8, "x_perm_sf"), _p(ws),
+                                        ws.numel(), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# 4-bit experts
+# ---------------------------------------------------------------------------
+
+def quantize_weights_w4(w: torch.Tensor, group: int = 128, stream=None):
+    """4-bit codes and bf16 group scales of weights [n, rows, cols] (contraction
+    axis = cols): (codes uint8 [n, rows/16, cols/128, 1024], scales bf16 [n, rows/16,
+    cols/128, 16, 128/group]), rows and columns rounded up to whole blocks."""
+    if w.dim() == 2:
+        w = w.unsqueeze(0)
+    n, rows, cols = w.shape
+    if w.dtype not in _DTYPE_CODES:
+        raise ValueError(f"w has dtype {w.dtype}, expected torch.float32 or torch.bfloat16")
+    if group not in (32, 64, 128):
+        raise MoEError(2, f"group {group} is none of 32, 64, 128")
+    _here(w)
+    rb, cb = -(-rows // 16), -(-cols // 128)
+    q = torch.empty((n, rb, cb, 1024), dtype=torch.uint8, device=w.device)
+    sc = torch.empty((n, rb, cb, 16, 128 // group), dtype=torch.bfloat16, device=w.device)
+    _check(lib().moe_quantize_weights_w4(n, rows, cols, group, _DTYPE_CODES[w.dtype],
+                                         _p(w, name="w"), _p(q), _p(sc), _stream(stream)))
+    return q, sc
+
+
+def _w4(pair, n, rows, cols, group, name):
+    """Pointers of a (codes, scales) pair whose sizes are checked."""
+    q, sc = pair
+    blocks = n * -(-rows // 16) * -(-cols // 128)
+    if q.numel() != blocks * 1024 or sc.numel() != blocks * 2048 // group:
+        raise ValueError(f"{name}: codes of {q.numel()} and scales of {sc.numel()} values do not "
+                         f"hold {n} matrices [{rows}, {cols}] in groups of {group}")
+    return _p(q, torch.uint8, name), _p(sc, torch.bfloat16, name)
+
+
+def expert_gate_up_w4(shape, group, x, row_token, w1, w3, offsets, h, ws, stream=None):
+    """w1, w3: (codes, scales) pairs from quantize_weights_w4; row_token None: x is
+    x_perm."""
+    dt = torch_dtype(shape)
+    _here(x, w1[0], w3[0], offsets, h, ws)
+    q1, s1 = _w4(w1, shape.N, shape.I, shape.d, group, "w1")
+    q3, s3 = _w4(w3, shape.N, shape.I, shape.d, group, "w3")
+    _check(lib().moe_expert_gate_up_w4(ctypes.byref(shape), group, _p(x, dt, "x"),
+                                       _p(row_token, torch.int32, "row_token"), q1, s1, q3, s3,
+                                       _p(offsets, torch.int32, "offsets"), _p(h, dt, "h"),
+                                       _p(ws), ws.numel(), _stream(stream)))
+
+
+def expert_down_w4(shape, group, h, w2, offsets, y_perm, ws, stream=None):
+    dt = torch_dtype(shape)
+    _here(h, w2[0], offsets, y_perm, ws)
+    q2, s2 = _w4(w2, shape.N, shape.d, shape.I, group, "w2")
+    _check(lib().moe_expert_down_w4(ctypes.byref(shape), group, _p(h, dt, "h"), q2, s2,
+                                    _p(offsets, torch.int32, "offsets"),
+                                    _p(y_perm, dt, "y_perm"), _p(ws), ws.numel(),
+                                    _stream(stream)))
+
+
+def forward_w4(buf: "LayerBuffers", group, x, w_router, w1, w3, w2, bias, gamma=1.0,
+               logit_offset=None, stream=None):
+    """The layer with 4-bit experts (decode batches): w1, w3, w2 are (codes, scales)
+    pairs in groups of `group`; no x_perm copy."""
+    s = buf.shape
+    route_dispatch(s, x, w_router, bias, buf.ws, buf.topk_idx, buf.topk_gate, buf.counts,
+                   buf.n_ffn, buf.offsets, buf.row_token, buf.slot_pos,
+                   logit_offset=logit_offset, probs_out=buf.probs, stream=stream)
+    expert_gate_up_w4(s, group, x, buf.row_token, w1, w3, buf.offsets, buf.h, buf.ws,
+                      stream=stream)
+    expert_down_w4(s, group, buf.h, w2, buf.offsets, buf.y_perm, buf.ws, stream=stream)
+    combine(s, x, buf.y_perm, buf.topk_idx, buf.topk_gate, buf.slot_pos, gamma, buf.out,
+            stream=stream)
+    return buf.out
+
+
+# ---------------------------------------------------------------------------
+# Residual RMS norm in front of the layer
+# ---------------------------------------------------------------------------
+
+def rmsnorm(x, weight, eps, y, residual=None, sum_out=None, inv_rms=None, y_q=None, y_sf=None,
+            stream=None):
+    """y = RMS norm of x (+ residual) times weight; sum_out receives x + residual,
+    inv_rms the row factors, y_q and y_sf the rounded y in MXFP8.  y may be None
+    when y_q is given."""
+    T, d, code = _rows(x)
+    dt = x.dtype
+    _here(x, weight, y, residual, sum_out, inv_rms, y_q, y_sf)
+    _same(x, (("residual", residual), ("sum_out", sum_out), ("y", y)))
+    _size(weight, d, "weight")
+    _size(inv_rms, T, "inv_rms")
+    _size(y_q, T * d, "y_q")
+    _size(y_sf, T * (d // 32), "y_sf")
+    _check(lib().moe_rmsnorm(T, d, code, _p(x, dt, "x"), _p(residual, dt, "residual"),
+                             _p(weight, dt, "weight"), eps, _p(sum_out, dt, "sum_out"),
+                             _p(y, dt, "y"), _p(inv_rms, torch.float32, "inv_rms"),
+                             _p(y_q, torch.uint8, "y_q"), _p(y_sf, torch.uint8, "y_sf"),
+                             _stream(stream)))
+
+
+def new_rmsnorm_workspace(T: int, d: int, device="cuda") -> torch.Tensor:
+    n = lib().moe_rmsnorm_workspace_bytes(T, d)
+    if n == 0:
+        raise MoEError(1, f"bad shape T={T} d={d}")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def rmsnorm_backward(s, weight, inv_rms, dy, dx, dweight, ws, dsum=None, stream=None):
+    """Gradients of rmsnorm: s is its sum_out (x without a residual), dsum the
+    gradient along the residual stream; dx is the gradient of x and of residual."""
+    T, d, code = _rows(s)
+    dt = s.dtype
+    _here(s, weight, inv_rms, dy, dx, dweight, ws, dsum)
+    _same(s, (("dy", dy), ("dx", dx), ("dsum", dsum)))
+    _size(weight, d, "weight")
+    _size(dweight, d, "dweight")
+    _size(inv_rms, T, "inv_rms")
+    _check(lib().moe_rmsnorm_backward(T, d, code, _p(s, dt, "s"), _p(weight, dt, "weight"),
+                                      _p(inv_rms, torch.float32, "inv_rms"), _p(dy, dt, "dy"),
+                                      _p(dsum, dt, "dsum"), _p(dx, dt, "dx"),
+                                      _p(dweight, dt, "dweight"), _p(ws), ws.numel(),
+                                      _stream(stream)))
+
+
+class PreNormBuffers:
+    """Buffers of the residual RMS norm in front of a layer, allocated once by torch:
+    the sum, its norm y (the layer's x), the row factors, with mx the MXFP8 codes and
+    scales of y (forward_mxfp8's x_q), with train the gradients and their workspace."""
+
+    def __init__(self, shape: Shape, device="cuda", mx=False, train=False):
+        T, d, dt = shape.T, shape.d, torch_dtype(shape)
+        kw = dict(device=device)
+        self.s = torch.empty((T, d), dtype=dt, **kw)
+        self.y = torch.empty((T, d), dtype=dt, **kw)
+        self.inv_rms = torch.empty(T, dtype=torch.float32, **kw)
+        self.x_q = (torch.empty((T, d), dtype=torch.uint8, **kw),
+                    torch.empty((T, d // 32), dtype=torch.uint8, **kw)) if mx else None
+        if train:
+            self.dx = torch.empty((T, d), dtype=dt, **kw)
+            self.dweight = torch.empty(d, dtype=dt, **kw)
+            self.ws = new_rmsnorm_workspace(T, d, device)
+
+
+def prenorm(nb: PreNormBuffers, x, residual, weight, eps=1e-5, stream=None):
+    """nb.s = x + residual and nb.y = its RMS norm times weight; returns nb.y, the x of
+    forward, forward_w4, forward_train or (with nb.x_q) forward_mxfp8."""
+    q, sf = nb.x_q if nb.x_q is not None else (None, None)
+    rmsnorm(x, weight, eps, nb.y, residual=residual, sum_out=nb.s, inv_rms=nb.inv_rms, y_q=q,
+            y_sf=sf, stream=stream)
+    return nb.y
+
+
+def prenorm_backward(nb: PreNormBuffers, weight, dy, dsum=None, stream=None):
+    """Gradients of prenorm from dy (backward's dx) and dsum, the gradient that reaches
+    nb.s along the residual stream: nb.dx (of x and of residual) and nb.dweight."""
+    rmsnorm_backward(nb.s, weight, nb.inv_rms, dy, nb.dx, nb.dweight, nb.ws, dsum=dsum,
+                     stream=stream)
+    return nb.dx
+
+
+# ---------------------------------------------------------------------------
+# Global gradient norm and clipping
+# ---------------------------------------------------------------------------
+
+class _Grad(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("dtype", ctypes.c_int32)]
+
+
+class GradientList:
+    """Gradient tensors (fp32 or bf16, contiguous, on one device) taken as one vector,
+    with the workspace of their norm.  out: where the clipped gradients go (by
+    default in place).  The list holds the tensors; make a new one when they change."""
+
+    def __init__(self, tensors, out=None, stream=None):
+        self.tensors = list(tensors)
+        self.out = self.tensors if out is None else list(out)
+        if len(self.out) != len(self.tensors):
+            raise ValueError(f"{len(self.tensors)} gradients, but {len(self.out)} outputs")
+        n = len(self.tensors)
+        self.table = (_Grad * max(n, 1))()
+        for i, (g, o) in enumerate(zip(self.tensors, self.out)):
+            if g.dtype not in _DTYPE_CODES:
+                raise ValueError(f"gradient {i} has dtype {g.dtype}, expected torch.float32 or "
+                                 "torch.bfloat16")
+            if o.numel() != g.numel():
+                raise ValueError(f"gradient {i} has {g.numel()} elements, its output {o.numel()}")
+            _p(o, g.dtype, f"output {i}")
+            _p(g, None, f"gradient {i}")
+            self.table[i] = _Grad(g.data_ptr(), o.data_ptr(), g.numel(), _DTYPE_CODES[g.dtype])
+        devices = {t.device for t in self.tensors + self.out}
+        if len(devices) > 1:
+            raise ValueError(f"gradients on several devices: {sorted(map(str, devices))}")
+        self._check_overlap()
+        self.device = devices.pop() if devices else torch.device("cuda",
+                                                                 torch.cuda.current_device())
+        ws_bytes = lib().moe_grad_workspace_bytes(n)
+        self.ws = torch.empty(ws_bytes, dtype=torch.uint8, device=self.device)
+        _here(self.ws)
+        _check(lib().moe_workspace_init(_p(self.ws), ws_bytes, _stream(stream)))
+
+    def _check_overlap(self):
+        """Every element is written once, and only from its own gradient."""
+        spans = []
+        for i, (g, o) in enumerate(zip(self.tensors, self.out)):
+            size = g.numel() * g.element_size()
+            if size:
+                spans.append((o.data_ptr(), o.data_ptr() + size, i, True))
+                if g.data_ptr() != o.data_ptr():
+                    spans.append((g.data_ptr(), g.data_ptr() + size, i, False))
+        spans.sort()
+        end = wrote = 0  # furthest end so far, of any span and of the written ones
+        for a, b, i, write in spans:
+            if a < (end if write else wrote):
+                raise ValueError(f"gradient {i} overlaps another tensor of the list")
+            end = max(end, b)
+            wrote = max(wrote, b) if write else wrote
+
+
+def gradient_norm(grads: GradientList, norm, stream=None):
+    """norm[0] = the 2-norm of all gradients together (fp32, on the device)."""
+    _here(grads.ws, norm)
+    _size(norm, 1, "norm")
+    _check(lib().moe_grad_norm(len(grads.tensors), grads.table, _p(norm, torch.float32, "norm"),
+                               _p(grads.ws), grads.ws.numel(), _stream(stream)))
+    return norm
+
+
+def clip_gradients(grads: GradientList, max_norm, norm, stream=None):
+    """Scales the gradients by min(1, max_norm / (norm + 1e-6)) into grads.out, with
+    their global norm, which is left in norm[0]."""
+    gradient_norm(grads, norm, stream=stream)
+    _check(lib().moe_grad_clip(len(grads.tensors), grads.table, float(max_norm),
+                               _p(norm, torch.float32, "norm"), _stream(stream)))
+    return norm
 
 
 def workspace_bytes(shape: Shape) -> int:

@@ -1,0 +1,203 @@
+// Global norm of a list of gradient tensors and clipping to it:
+//   norm = sqrt(sum over every tensor and element of g^2)
+//   g' = round(g * min(1, max_norm / (norm + 1e-6)))
+// Bound by memory: the norm reads every element once, the clipping reads and
+// writes it once more.
+//
+// Squares and the eight (bf16) or four (fp32) of a vector are summed in fp32,
+// vectors in fp64 (one conversion and addition per 16 bytes, far below the
+// memory time), so the sum over billions of elements keeps fp32 accuracy.  A CTA
+// sums its chunks in a fixed order and the last CTA to finish adds the CTAs'
+// sums in a fixed order: the norm is bit-reproducible.
+#pragma once
+
+#include "common.cuh"
+
+namespace moe {
+
+constexpr int kClipTensors = 96;   // tensors of one launch: the table is a kernel argument
+constexpr int kClipThreads = 256;
+constexpr int kClipVecs = 4;       // 16-byte vectors per thread and chunk
+constexpr int kClipChunkVecs = kClipThreads * kClipVecs;  // one chunk: 16 KiB
+constexpr int kClipMaxCtas = 148 * 8;
+
+struct ClipTable {
+  const void* in[kClipTensors];
+  void* out[kClipTensors];
+  long long numel[kClipTensors];
+  long long first[kClipTensors + 1];  // first chunk of each tensor, and the total
+  uint32_t bf16[kClipTensors / 32];   // bit i: tensor i holds bf16
+  int n;
+};
+
+// Elements before the first 16-byte boundary of a tensor's data.
+template <typename T>
+MOE_DEV long long clip_head(const void* p, long long n) {
+  const uintptr_t off = reinterpret_cast<uintptr_t>(p) & 15;
+  const long long h = off ? (long long)((16 - off) / sizeof(T)) : 0;
+  return h < n ? h : n;
+}
+
+MOE_DEV int clip_find(const ClipTable& tab, long long c) {
+  int lo = 0, hi = tab.n;  // first[lo] <= c < first[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (tab.first[mid] <= c) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// This thread's share of the squares of one chunk.  Chunk 0 of a tensor also
+// takes the elements before the first boundary and behind the last full vector.
+template <typename T>
+MOE_DEV double clip_squares(const T* p, long long n, long long chunk) {
+  constexpr int VN = Vec16<T>::kN;
+  const long long head = clip_head<T>(p, n), nvec = (n - head) / VN;
+  const uint4* body = reinterpret_cast<const uint4*>(p + head);
+  const long long v0 = chunk * kClipChunkVecs + threadIdx.x;
+  uint4 raw[kClipVecs];
+#pragma unroll
+  for (int i = 0; i < kClipVecs; ++i) {
+    const long long v = v0 + i * kClipThreads;
+    raw[i] = v < nvec ? __ldg(body + v) : make_uint4(0, 0, 0, 0);
+  }
+  double acc = 0.0;
+#pragma unroll
+  for (int i = 0; i < kClipVecs; ++i) {
+    float f[VN], q = 0.f;
+    unpack16(raw[i], f, T());
+#pragma unroll
+    for (int k = 0; k < VN; ++k) q = fmaf(f[k], f[k], q);
+    acc += (double)q;
+  }
+  if (chunk == 0) {
+    const long long tail = head + nvec * VN;
+    if (threadIdx.x < head) {
+      const float f = Cvt<T>::to_f(p[threadIdx.x]);
+      acc += (double)(f * f);
+    }
+    if (tail + threadIdx.x < n) {
+      const float f = Cvt<T>::to_f(p[tail + threadIdx.x]);
+      acc += (double)(f * f);
+    }
+  }
+  return acc;
+}
+
+// Partial sums of one table's chunks go to part[base + CTA]; the last CTA of
+// the launch that holds the list's end adds all of them and writes the norm.
+static __global__ void __launch_bounds__(kClipThreads)
+grad_norm_kernel(const __grid_constant__ ClipTable tab, double* part, int base, int total_parts,
+                 unsigned int* ticket, float* norm) {
+  pdl_trigger();
+  pdl_wait();
+  __shared__ double warp_sum[kClipThreads / 32];
+  __shared__ bool last;
+  const long long chunks = tab.first[tab.n];
+  double acc = 0.0;
+  for (long long c = blockIdx.x; c < chunks; c += gridDim.x) {
+    const int i = clip_find(tab, c);
+    const long long k = c - tab.first[i];
+    if (tab.bf16[i >> 5] >> (i & 31) & 1)
+      acc += clip_squares(static_cast<const __nv_bfloat16*>(tab.in[i]), tab.numel[i], k);
+    else
+      acc += clip_squares(static_cast<const float*>(tab.in[i]), tab.numel[i], k);
+  }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto block_sum = [&](double v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    __syncthreads();
+    if (lane == 0) warp_sum[warp] = v;
+    __syncthreads();
+    double t = 0.0;
+#pragma unroll
+    for (int j = 0; j < kClipThreads / 32; ++j) t += warp_sum[j];
+    return t;
+  };
+  const double sum = block_sum(acc);
+  if (threadIdx.x == 0) {
+    part[base + blockIdx.x] = sum;
+    __threadfence();
+    last = norm && atomicAdd(ticket, 1u) == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  double t = 0.0;
+  for (int j = threadIdx.x; j < total_parts; j += kClipThreads) t += __ldcg(part + j);
+  t = block_sum(t);
+  if (threadIdx.x == 0) {
+    *norm = (float)sqrt(t);
+    *ticket = 0;  // ready for the next call on this workspace
+  }
+}
+
+template <typename T>
+MOE_DEV void clip_scale(const T* in, T* out, long long n, long long chunk, float coef) {
+  constexpr int VN = Vec16<T>::kN;
+  const long long head = clip_head<T>(in, n);
+  const bool aligned = clip_head<T>(out, n) == head;  // both reach a boundary together
+  const long long nvec = (n - head) / VN;
+  const long long v0 = chunk * kClipChunkVecs + threadIdx.x;
+  if (aligned) {
+    const uint4* src = reinterpret_cast<const uint4*>(in + head);
+    uint4* dst = reinterpret_cast<uint4*>(out + head);
+    uint4 raw[kClipVecs];
+#pragma unroll
+    for (int i = 0; i < kClipVecs; ++i) {
+      const long long v = v0 + i * kClipThreads;
+      if (v < nvec) raw[i] = src[v];
+    }
+#pragma unroll
+    for (int i = 0; i < kClipVecs; ++i) {
+      const long long v = v0 + i * kClipThreads;
+      if (v >= nvec) continue;
+      float f[VN];
+      unpack16(raw[i], f, T());
+#pragma unroll
+      for (int k = 0; k < VN; ++k) f[k] *= coef;
+      dst[v] = pack16(f, T());
+    }
+  } else {  // out starts elsewhere in its 16 bytes: element by element, the same chunks
+    for (int i = 0; i < kClipVecs; ++i) {
+      const long long v = v0 + i * kClipThreads;
+      if (v >= nvec) continue;
+      for (int k = 0; k < VN; ++k) {
+        const long long j = head + v * VN + k;
+        out[j] = Cvt<T>::from_f(Cvt<T>::to_f(in[j]) * coef);
+      }
+    }
+  }
+  if (chunk == 0) {
+    const long long tail = head + nvec * VN;
+    if (threadIdx.x < head)
+      out[threadIdx.x] = Cvt<T>::from_f(Cvt<T>::to_f(in[threadIdx.x]) * coef);
+    if (tail + threadIdx.x < n)
+      out[tail + threadIdx.x] = Cvt<T>::from_f(Cvt<T>::to_f(in[tail + threadIdx.x]) * coef);
+  }
+}
+
+// in_place: every out is its in, so a factor of 1 leaves nothing to write.
+static __global__ void __launch_bounds__(kClipThreads)
+grad_clip_kernel(const __grid_constant__ ClipTable tab, float max_norm, bool in_place,
+                 const float* __restrict__ norm) {
+  pdl_trigger();
+  pdl_wait();
+  float coef = max_norm / (*norm + 1e-6f);
+  if (coef > 1.0f) coef = 1.0f;  // NaN stays NaN
+  if (in_place && coef == 1.0f) return;
+  const long long chunks = tab.first[tab.n];
+  for (long long c = blockIdx.x; c < chunks; c += gridDim.x) {
+    const int i = clip_find(tab, c);
+    const long long k = c - tab.first[i];
+    if (tab.bf16[i >> 5] >> (i & 31) & 1)
+      clip_scale(static_cast<const __nv_bfloat16*>(tab.in[i]),
+                 static_cast<__nv_bfloat16*>(tab.out[i]), tab.numel[i], k, coef);
+    else
+      clip_scale(static_cast<const float*>(tab.in[i]), static_cast<float*>(tab.out[i]),
+                 tab.numel[i], k, coef);
+  }
+}
+
+}  // namespace moe

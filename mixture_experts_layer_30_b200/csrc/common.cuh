@@ -190,7 +190,7 @@ MOE_DEV int find_expert(const int* prefix, int N, int c) {
 // One CTA per 128 x 64 bf16 tile (16 KiB): copies tile (m, rb, cb) of the
 // row-major matrices [rows, cols] to position (m*rows/128 + rb)*cols/64 + cb
 // of the tiled order, row-major inside the tile.  16-byte vectors.
-__global__ void __launch_bounds__(256)
+static __global__ void __launch_bounds__(256)
 pack_tiles_kernel(const uint4* __restrict__ src, int rows, int cols, uint4* __restrict__ dst) {
   pdl_trigger();
   pdl_wait();

@@ -12,6 +12,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "moe.h"
+#include "api_shared.h"
 #include "common.cuh"
 #include "route.cuh"
 #include "permute.cuh"
@@ -26,7 +27,7 @@
 
 namespace {
 
-thread_local char g_err[512] = "";
+thread_local char g_err[moe::api::kErrorBytes] = "";
 
 // NVTX range over one C-ABI call (the enqueue on the host; profilers place the
 // call's kernels under it).  Header-only NVTX: a no-op unless a tool is attached.
@@ -860,6 +861,43 @@ moe_status moe_permute_mxfp8(const moe_shape* shape, const void* x, const int32_
   return MOE_OK;
 }
 
+moe_status moe_permute_mxfp8_rows(const moe_shape* shape, const void* x_q, const void* x_sf,
+                                  const int32_t* topk_idx, const int32_t* counts,
+                                  int32_t* offsets, int32_t* row_token, int32_t* slot_pos,
+                                  void* x_perm_q, void* x_perm_sf, void* ws, size_t ws_bytes,
+                                  void* stream) {
+  g_err[0] = 0;
+  NvtxRange nvtx_range_("moe_permute_mxfp8_rows");
+  MOE_TRY(check_mxfp8_shape(shape));
+  const moe_shape& s = *shape;
+  WsLayout L;
+  MOE_TRY(check_ws(s, ws, ws_bytes, &L));
+  MOE_TRY(need(offsets, "offsets", 4));
+  if (s.T > 0) {
+    MOE_TRY(need(x_q, "x_q", 16));
+    MOE_TRY(need(x_sf, "x_sf", 16));
+    MOE_TRY(need(topk_idx, "topk_idx", 4));
+    MOE_TRY(need(row_token, "row_token", 4));
+    MOE_TRY(need(slot_pos, "slot_pos", 4));
+    MOE_TRY(need(x_perm_q, "x_perm_q", 16));
+    MOE_TRY(need(x_perm_sf, "x_perm_sf", 16));
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  MOE_TRY(permute_impl<__nv_bfloat16>(s, nullptr, topk_idx, counts, offsets, row_token, slot_pos,
+                                      nullptr, ws, L, st));
+  if (s.T > 0) {
+    const long long items = (long long)s.T * ((s.d + moe::kRowPiece - 1) / moe::kRowPiece + 1);
+    if ((items + 7) / 8 > 0x7fffffffLL)
+      return fail(MOE_ERR_UNSUPPORTED, "T=%d, d=%d: too many row pieces", s.T, s.d);
+    moe::launch_pdl(moe::gather_rows_mxfp8_kernel, dim3((unsigned)((items + 7) / 8)), dim3(256),
+                    0, st, static_cast<const uint8_t*>(x_q), static_cast<const uint8_t*>(x_sf),
+                    slot_pos, s.T, s.K, s.d, static_cast<uint8_t*>(x_perm_q),
+                    static_cast<uint8_t*>(x_perm_sf));
+    MOE_TRY(check_launch("8-bit row dispatch copy"));
+  }
+  return MOE_OK;
+}
+
 moe_status moe_expert_gate_up_mxfp8(const moe_shape* shape, const void* x_perm_q,
                                     const void* x_perm_sf, const void* w1_q, const void* w1_sf,
                                     const void* w3_q, const void* w3_sf, const int32_t* offsets,
@@ -1424,3 +1462,20 @@ moe_status moe_debug_set_pipeline(uint64_t wait_limit_ns, int32_t stall_first_fi
 }
 
 }  // extern "C"
+
+// --- shared with the other translation units ---------------------------------
+namespace moe {
+namespace api {
+
+char* error_buffer() { return g_err; }
+
+moe_status layer_status(const moe_shape* shape, void* ws, size_t ws_bytes, uint32_t** status) {
+  MOE_TRY(validate_shape(shape));
+  WsLayout L;
+  MOE_TRY(check_ws(*shape, ws, ws_bytes, &L));
+  *status = at<uint32_t>(ws, L.status);
+  return MOE_OK;
+}
+
+}  // namespace api
+}  // namespace moe

@@ -1,0 +1,325 @@
+// Root-mean-square norm with the residual's addition, its MXFP8 output, and its
+// backward pass.  Per token row t over d columns:
+//   s = round(x + residual)            (storage type; s = x without a residual)
+//   inv = 1 / sqrt(mean_j s_j^2 + eps)
+//   y_j = round(s_j inv w_j),  q, sf = MXFP8(y)
+// The norm is taken of the rounded sum, so y is a function of what is kept (s,
+// inv) and the backward pass recomputes the same xhat = s inv.  Sums are fp32.
+//
+// Backward, for dy = dL/dy and dsum = dL/ds through the residual stream:
+//   c = mean_j(w_j dy_j xhat_j),  dx_j = inv (w_j dy_j - xhat_j c) + dsum_j
+//   dw_j = sum_t dy_tj xhat_tj
+// (dx is the gradient of x and of the residual: both enter by the sum.)
+//
+// Both passes are bound by memory: a row is read once, kept in registers over
+// the reduction, and written once.
+#pragma once
+
+#include "common.cuh"
+#include "quant.cuh"
+
+namespace moe {
+
+// Sum of v over the threads of one row (blockDim.x of them, a multiple of 32)
+// in a fixed order; red: shared scratch of 32 floats per row of the block.
+MOE_DEV float row_sum(float v, float* red) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const int nw = blockDim.x >> 5;
+  if (nw == 1) return v;
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float r = (threadIdx.x & 31) < nw ? red[threadIdx.x & 31] : 0.f;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+  return r;
+}
+
+// One vector of the output: y = s inv w rounded, and (kMx) its share of the
+// MXFP8 block.  A 32-column block is four vectors of four neighbouring lanes;
+// the codes are those of the rounded y, so a later quantisation of y gives the
+// same bytes.  Every lane of the warp calls.
+template <typename T, bool kMx>
+MOE_DEV void norm_emit(const float* f, float inv, const uint4& wraw, bool active, int v, size_t row,
+                       int d, T* y, uint8_t* yq, uint8_t* ysf) {
+  constexpr int VN = Vec16<T>::kN;
+  float w[VN], o[VN];
+  unpack16(wraw, w, T());
+#pragma unroll
+  for (int i = 0; i < VN; ++i) o[i] = f[i] * inv * w[i];
+  const uint4 packed = pack16(o, T());
+  if (active && y) reinterpret_cast<uint4*>(y + row * d)[v] = packed;
+  if constexpr (kMx) {
+    unpack16(packed, o, T());
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < VN; ++i) amax = fmaxf(amax, fabsf(o[i]));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    const int s = mx_scale_exp(amax);
+    const float is = mx_inv_scale(s);
+    uint32_t q[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      q[h] = (uint32_t)mx_quant_inv(o[4 * h], is) | ((uint32_t)mx_quant_inv(o[4 * h + 1], is) << 8) |
+             ((uint32_t)mx_quant_inv(o[4 * h + 2], is) << 16) |
+             ((uint32_t)mx_quant_inv(o[4 * h + 3], is) << 24);
+    if (active) {
+      reinterpret_cast<uint2*>(yq + row * d)[v] = make_uint2(q[0], q[1]);
+      if ((v & 3) == 0) ysf[row * (d / 32) + (v >> 2)] = mx_scale_byte(s);
+    }
+  }
+}
+
+// One row per blockDim.x threads, blockDim.y rows a CTA; VPT vectors of a row
+// per thread in registers, or VPT = 0: rows longer than the registers hold are
+// read a second time (from the stored sum when there is a residual).  Outputs
+// may share memory with inputs of the same row: a thread reads its vectors
+// before it writes them.
+template <typename T, int VPT, bool kRes, bool kMx>
+__global__ void __launch_bounds__(1024)
+rmsnorm_kernel(const T* x, const T* res, const T* __restrict__ w, float eps, int rows, int d,
+               T* sum_out, T* y, float* inv_out, uint8_t* yq, uint8_t* ysf) {
+  pdl_trigger();
+  pdl_wait();
+  constexpr int VN = Vec16<T>::kN;
+  __shared__ float red[32 * 4];
+  const int row_i = blockIdx.x * blockDim.y + threadIdx.y;
+  const bool live = row_i < rows;
+  const size_t row = live ? row_i : 0;
+  const int nvec = d / VN, tid = threadIdx.x, step = blockDim.x;
+  const uint4* xv = reinterpret_cast<const uint4*>(x + row * d);
+  const uint4* rv = kRes ? reinterpret_cast<const uint4*>(res + row * d) : nullptr;
+  uint4* sv = kRes ? reinterpret_cast<uint4*>(sum_out + row * d) : nullptr;
+  const uint4* wv = reinterpret_cast<const uint4*>(w);
+  float ss = 0.f;
+  // s of one vector: the rounded sum, stored when there is a residual
+  auto take = [&](const uint4& a, const uint4& b, int v, float* f) -> uint4 {
+    unpack16(a, f, T());
+    uint4 packed = a;
+    if constexpr (kRes) {
+      float g[VN];
+      unpack16(b, g, T());
+#pragma unroll
+      for (int i = 0; i < VN; ++i) f[i] += g[i];
+      packed = pack16(f, T());
+      unpack16(packed, f, T());
+      sv[v] = packed;
+    }
+#pragma unroll
+    for (int i = 0; i < VN; ++i) ss = fmaf(f[i], f[i], ss);
+    return packed;
+  };
+  if constexpr (VPT > 0) {
+    uint4 a[VPT], b[VPT], wr[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = tid + i * step;
+      a[i] = make_uint4(0, 0, 0, 0);
+      b[i] = wr[i] = a[i];
+      if (live && v < nvec) {
+        a[i] = xv[v];
+        if constexpr (kRes) b[i] = rv[v];
+        wr[i] = __ldg(wv + v);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = tid + i * step;
+      float f[VN];
+      if (live && v < nvec) a[i] = take(a[i], b[i], v, f);
+    }
+    ss = row_sum(ss, red + 32 * threadIdx.y);
+    const float inv = 1.0f / sqrtf(ss / (float)d + eps);
+    if (live && tid == 0 && inv_out) inv_out[row] = inv;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = tid + i * step;
+      float f[VN];
+      unpack16(a[i], f, T());
+      norm_emit<T, kMx>(f, inv, wr[i], live && v < nvec, v, row, d, y, yq, ysf);
+    }
+  } else {
+    for (int v = tid; v < nvec; v += step) {
+      float f[VN];
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      if (live) take(xv[v], kRes ? rv[v] : zero, v, f);
+    }
+    ss = row_sum(ss, red + 32 * threadIdx.y);
+    const float inv = 1.0f / sqrtf(ss / (float)d + eps);
+    if (live && tid == 0 && inv_out) inv_out[row] = inv;
+    const uint4* again = kRes ? sv : xv;
+    for (int v0 = 0; v0 < nvec; v0 += step) {
+      const int v = v0 + tid;
+      const bool active = live && v < nvec;
+      uint4 a = make_uint4(0, 0, 0, 0), wr = a;
+      if (active) {
+        a = again[v];
+        wr = __ldg(wv + v);
+      }
+      float f[VN];
+      unpack16(a, f, T());
+      norm_emit<T, kMx>(f, inv, wr, active, v, row, d, y, yq, ysf);
+    }
+  }
+}
+
+// Backward: CTA c takes rows c, c + grid, ...; its threads own the same columns
+// in every row, so dw accumulates in registers and the CTA writes one fp32
+// partial row.  The next row is loaded before the reduction of this one.
+// VPT = 0: rows longer than the registers hold; the partial row is kept in
+// global memory instead (each thread adds to its own columns).
+template <typename T, int VPT, bool kSum>
+__global__ void __launch_bounds__(512)
+rmsnorm_bwd_kernel(const T* s, const T* __restrict__ w, const float* __restrict__ inv_rms,
+                   const T* dy, const T* dsum, int rows, int d, T* dx, float* __restrict__ part) {
+  pdl_trigger();
+  pdl_wait();
+  constexpr int VN = Vec16<T>::kN;
+  __shared__ float red[2][32];
+  const int nvec = d / VN, tid = threadIdx.x, step = blockDim.x;
+  const uint4* wv = reinterpret_cast<const uint4*>(w);
+  float* mine = part + (size_t)blockIdx.x * d;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  int flip = 0;
+  if constexpr (VPT > 0) {
+    uint4 wr[VPT], sa[VPT], ya[VPT];
+    float dw[VPT][VN];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = tid + i * step;
+      wr[i] = sa[i] = ya[i] = zero;
+      if (v < nvec) {
+        wr[i] = __ldg(wv + v);
+        if (blockIdx.x < rows) {
+          sa[i] = reinterpret_cast<const uint4*>(s + (size_t)blockIdx.x * d)[v];
+          ya[i] = reinterpret_cast<const uint4*>(dy + (size_t)blockIdx.x * d)[v];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < VN; ++k) dw[i][k] = 0.f;
+    }
+    for (int r = blockIdx.x; r < rows; r += gridDim.x) {
+      uint4 cs[VPT], cy[VPT], add[VPT];
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int v = tid + i * step;
+        cs[i] = sa[i];
+        cy[i] = ya[i];
+        if (v < nvec) {
+          if constexpr (kSum) add[i] = reinterpret_cast<const uint4*>(dsum + (size_t)r * d)[v];
+          if (r + (int)gridDim.x < rows) {
+            const size_t nr = (size_t)(r + gridDim.x) * d;
+            sa[i] = reinterpret_cast<const uint4*>(s + nr)[v];
+            ya[i] = reinterpret_cast<const uint4*>(dy + nr)[v];
+          }
+        }
+      }
+      const float inv = inv_rms[r];
+      float c = 0.f;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        float f[VN], g[VN], ww[VN];
+        unpack16(cs[i], f, T());
+        unpack16(cy[i], g, T());
+        unpack16(wr[i], ww, T());
+#pragma unroll
+        for (int k = 0; k < VN; ++k) {
+          const float p = g[k] * (f[k] * inv);
+          c = fmaf(ww[k], p, c);
+          dw[i][k] += p;
+        }
+      }
+      c = row_sum(c, red[flip]) / (float)d;
+      flip ^= 1;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int v = tid + i * step;
+        if (v >= nvec) continue;
+        float f[VN], g[VN], ww[VN], o[VN];
+        unpack16(cs[i], f, T());
+        unpack16(cy[i], g, T());
+        unpack16(wr[i], ww, T());
+        if constexpr (kSum) unpack16(add[i], o, T());
+#pragma unroll
+        for (int k = 0; k < VN; ++k) {
+          const float t = inv * (ww[k] * g[k] - f[k] * inv * c);
+          o[k] = kSum ? o[k] + t : t;
+        }
+        reinterpret_cast<uint4*>(dx + (size_t)r * d)[v] = pack16(o, T());
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = tid + i * step;
+      if (v >= nvec) continue;
+#pragma unroll
+      for (int k = 0; k < VN; k += 4)
+        reinterpret_cast<float4*>(mine)[(v * VN + k) / 4] =
+            make_float4(dw[i][k], dw[i][k + 1], dw[i][k + 2], dw[i][k + 3]);
+    }
+  } else {
+    for (int j = tid; j < nvec; j += step)
+#pragma unroll
+      for (int k = 0; k < VN; ++k) mine[j * VN + k] = 0.f;
+    for (int r = blockIdx.x; r < rows; r += gridDim.x) {
+      const uint4* srow = reinterpret_cast<const uint4*>(s + (size_t)r * d);
+      const uint4* yrow = reinterpret_cast<const uint4*>(dy + (size_t)r * d);
+      const float inv = inv_rms[r];
+      float c = 0.f;
+      for (int v = tid; v < nvec; v += step) {
+        float f[VN], g[VN], ww[VN];
+        unpack16(srow[v], f, T());
+        unpack16(yrow[v], g, T());
+        unpack16(__ldg(wv + v), ww, T());
+#pragma unroll
+        for (int k = 0; k < VN; ++k) {
+          const float p = g[k] * (f[k] * inv);
+          c = fmaf(ww[k], p, c);
+          mine[v * VN + k] += p;
+        }
+      }
+      c = row_sum(c, red[flip]) / (float)d;
+      flip ^= 1;
+      for (int v = tid; v < nvec; v += step) {
+        float f[VN], g[VN], ww[VN], o[VN];
+        unpack16(srow[v], f, T());
+        unpack16(yrow[v], g, T());
+        unpack16(__ldg(wv + v), ww, T());
+        if constexpr (kSum)
+          unpack16(reinterpret_cast<const uint4*>(dsum + (size_t)r * d)[v], o, T());
+#pragma unroll
+        for (int k = 0; k < VN; ++k) {
+          const float t = inv * (ww[k] * g[k] - f[k] * inv * c);
+          o[k] = kSum ? o[k] + t : t;
+        }
+        reinterpret_cast<uint4*>(dx + (size_t)r * d)[v] = pack16(o, T());
+      }
+    }
+  }
+}
+
+// dw[j] = sum over the n partial rows in a fixed order: 32 columns a CTA, 8
+// warps that each sum every eighth row, joined in warp order.  n = 0 gives 0.
+template <typename T>
+__global__ void __launch_bounds__(256)
+rmsnorm_dw_kernel(const float* __restrict__ part, int n, int d, T* __restrict__ dw) {
+  pdl_trigger();
+  pdl_wait();
+  __shared__ float acc[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int j = blockIdx.x * 32 + lane;
+  float v = 0.f;
+  if (j < d)
+    for (int r = warp; r < n; r += 8) v += part[(size_t)r * d + j];
+  acc[warp][lane] = v;
+  __syncthreads();
+  if (warp == 0 && j < d) {
+    float t = acc[0][lane];
+#pragma unroll
+    for (int k = 1; k < 8; ++k) t += acc[k][lane];
+    dw[j] = Cvt<T>::from_f(t);
+  }
+}
+
+}  // namespace moe

@@ -75,7 +75,7 @@ MOE_DEV int mx_quant_block_bf16(const uint4 (&in)[4], uint4 (&q)[2]) {
 // one 512-byte scale atom per tile: byte 16*(r % 32) + 4*(r / 32) + b holds
 // the scale of tile row r, 32-column block b (the replicated-lane order the
 // tensor memory scale copy expects).  One CTA per tile.
-__global__ void __launch_bounds__(256)
+static __global__ void __launch_bounds__(256)
 quantize_weights_mxfp8_kernel(const __nv_bfloat16* __restrict__ src, int rows, int cols,
                               uint8_t* __restrict__ dst_q, uint8_t* __restrict__ dst_sf) {
   pdl_trigger();
@@ -105,7 +105,7 @@ quantize_weights_mxfp8_kernel(const __nv_bfloat16* __restrict__ src, int rows, i
 // blocks b = lane, lane + 32, ...; every row of the token receives the E4M3
 // codes of x[t] (row-major [rows, d] bytes) and the block scales (row-major
 // [rows, d/32] bytes).
-__global__ void __launch_bounds__(256)
+static __global__ void __launch_bounds__(256)
 gather_quant_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restrict__ slot_pos,
                     int ntok, int K, int d, uint8_t* __restrict__ xq, uint8_t* __restrict__ xsf) {
   pdl_trigger();
@@ -140,6 +140,65 @@ gather_quant_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restri
           dq[0] = q[0];
           dq[1] = q[1];
           xsf[(size_t)row * nblk + b] = sb;
+        }
+      }
+    }
+  }
+}
+
+// Dispatch copy of rows that are held in 8 bits already: every routed row of
+// token t receives the token's E4M3 codes (d bytes) and block scales (d/32
+// bytes) unchanged.  Bound by memory: each token row is read once and written
+// to its FFN slots.  One warp copies one 2 KiB piece of one token's codes (four
+// 16-byte vectors a lane, held in registers while they are written to every
+// row), so a batch of few tokens still spreads over the SMs; the last piece of
+// a token is its scales (8-byte vectors: d % 256 == 0).
+constexpr int kRowPiece = 2048;
+static __global__ void __launch_bounds__(256)
+gather_rows_mxfp8_kernel(const uint8_t* __restrict__ xq, const uint8_t* __restrict__ xsf,
+                         const int32_t* __restrict__ slot_pos, int ntok, int K, int d,
+                         uint8_t* __restrict__ oq, uint8_t* __restrict__ osf) {
+  pdl_trigger();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int pieces = (d + kRowPiece - 1) / kRowPiece + 1;
+  const long long item = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  const long long t = item / pieces;
+  if (t >= ntok) return;
+  const int piece = (int)(item - t * pieces);
+  const bool scales = piece == pieces - 1;
+  uint4 v[4];
+  uint2 sv[4];
+  const int nsf = d / 256;          // 8-byte vectors of one row's scales
+  const int v0 = piece * (kRowPiece / 16), nvec = d / 16;
+  if (!scales) {
+    const uint4* src = reinterpret_cast<const uint4*>(xq + (size_t)t * d) + v0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (v0 + i * 32 + lane < nvec) v[i] = __ldg(src + i * 32 + lane);
+  }
+  for (int kb = 0; kb < K; kb += 32) {
+    const int my_row = kb + lane < K ? slot_pos[(size_t)t * K + kb + lane] : -1;
+    uint32_t has = __ballot_sync(0xffffffffu, my_row >= 0);
+    while (has) {
+      const int j = __ffs(has) - 1;
+      has &= has - 1;
+      const size_t row = (size_t)__shfl_sync(0xffffffffu, my_row, j);
+      if (!scales) {
+        uint4* dst = reinterpret_cast<uint4*>(oq + row * d) + v0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (v0 + i * 32 + lane < nvec) dst[i * 32 + lane] = v[i];
+      } else {
+        const uint2* src = reinterpret_cast<const uint2*>(xsf + (size_t)t * (d / 32));
+        uint2* dst = reinterpret_cast<uint2*>(osf + row * (d / 32));
+        for (int b = 0; b < nsf; b += 128) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (b + i * 32 + lane < nsf) sv[i] = __ldg(src + b + i * 32 + lane);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (b + i * 32 + lane < nsf) dst[b + i * 32 + lane] = sv[i];
         }
       }
     }
