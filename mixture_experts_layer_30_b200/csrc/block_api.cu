@@ -211,10 +211,37 @@ moe_status w4_simt(const moe_shape& s, const W4Args& a) {
       kGated ? "4-bit gate/up" : "4-bit down");
 }
 
+template <int GPS, bool kGated>
+moe_status w4_mma(const moe_shape& s, const W4Args& a) {
+  const moe::W4Problem p{{static_cast<const uint8_t*>(a.q0), static_cast<const uint8_t*>(a.q1)},
+                         {static_cast<const __nv_bfloat16*>(a.s0),
+                          static_cast<const __nv_bfloat16*>(a.s1)},
+                         static_cast<const __nv_bfloat16*>(a.a), a.a_rows, a.offsets, s.N,
+                         s.T * s.K, s.T, a.n_out, a.k_dim, static_cast<__nv_bfloat16*>(a.c),
+                         a.status};
+  const long long ctas = 2LL * sm_count();
+  const long long rb = moe::w4_row_blocks(a.n_out), units = kGated ? rb : (rb + 1) / 2;
+  // At most one chunk per touched expert and 32 rows: with too few pairs of row
+  // blocks for every CTA to have some, a CTA takes one pair in eight slices.
+  const long long max_rows = (long long)s.T * s.K;
+  const long long chunks = std::min<long long>(s.N, max_rows) + max_rows / moe::kW4MaxTokens;
+  const bool narrow = chunks * ((units + 1) / 2) < 2 * ctas;
+  const long long items = chunks * (narrow ? units : (units + 1) / 2);
+  const dim3 grid((unsigned)std::min(items, ctas));
+  return launched(moe::launch_pdl(narrow ? moe::w4_mma_kernel<GPS, kGated, 1>
+                                         : moe::w4_mma_kernel<GPS, kGated, 2>,
+                                  grid, dim3(moe::kW4Warps * 32), 0, a.st, p),
+                  kGated ? "4-bit gate/up" : "4-bit down");
+}
+
 template <bool kGated>
 moe_status w4_product(const moe_shape& s, const W4Args& a) {
-  if (s.dtype == MOE_BF16) return w4_simt<__nv_bfloat16, kGated>(s, a);
-  return w4_simt<float, kGated>(s, a);
+  if (s.dtype != MOE_BF16) return w4_simt<float, kGated>(s, a);
+  switch (a.gps) {
+    case 1: return w4_mma<1, kGated>(s, a);
+    case 2: return w4_mma<2, kGated>(s, a);
+    default: return w4_mma<4, kGated>(s, a);
+  }
 }
 
 // I is the contraction of the second half: its rows are read 16 bytes at a time.
