@@ -143,33 +143,48 @@ struct NormBwdArgs {
   cudaStream_t st;
 };
 
-template <typename T, int VPT>
-cudaError_t norm_bwd_launch(const NormBwdArgs& a, int threads) {
-  const dim3 grid((unsigned)norm_bwd_ctas(a.T));
-  auto go = [&](auto* kernel) {
-    return moe::launch_pdl(kernel, grid, dim3(threads), 0, a.st, static_cast<const T*>(a.s),
-                           static_cast<const T*>(a.w), a.inv, static_cast<const T*>(a.dy),
-                           static_cast<const T*>(a.dsum), a.T, a.d, static_cast<T*>(a.dx), a.part);
-  };
-  return a.dsum ? go(moe::rmsnorm_bwd_kernel<T, VPT, true>)
-                : go(moe::rmsnorm_bwd_kernel<T, VPT, false>);
+// threads of one row x groups; VPT = 0 takes no ring.  *ctas: partial rows written.
+template <typename T, int VPT, bool kSum>
+cudaError_t norm_bwd_launch(const NormBwdArgs& a, int threads, int groups, int* ctas) {
+  auto* kernel = moe::rmsnorm_bwd_kernel<T, VPT, kSum>;
+  const int smem = moe::kBwdDepth * (kSum ? 3 : 2) * VPT * threads * groups * 16;
+  // CTAs that an SM holds: by the ring, and by the 512 threads x 128 registers that the
+  // kernel may take
+  const int fit = smem ? (224 * 1024) / (smem + 2048) : 4;
+  const int per_sm = std::max(1, std::min({4, fit, 1024 / (threads * groups)}));
+  *ctas = std::min((a.T + groups - 1) / groups, std::min(sm_count() * per_sm, kNormBwdCtas));
+  if (smem + 2048 > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  return moe::launch_pdl(kernel, dim3(*ctas), dim3(threads, groups), smem, a.st,
+                         static_cast<const T*>(a.s), static_cast<const T*>(a.w), a.inv,
+                         static_cast<const T*>(a.dy), static_cast<const T*>(a.dsum), a.T, a.d,
+                         static_cast<T*>(a.dx), a.part);
+}
+
+template <typename T, bool kSum>
+cudaError_t norm_bwd_dispatch(const NormBwdArgs& a, int* ctas) {
+  const int nvec = a.d / moe::Vec16<T>::kN;
+  auto width = [&](int vpt) { return ((nvec + vpt - 1) / vpt + 31) / 32 * 32; };
+  // short rows: several to a CTA of 256 threads
+  auto groups = [&](int threads) { return std::max(1, std::min(8, 256 / threads)); };
+  if (width(1) <= 128) return norm_bwd_launch<T, 1, kSum>(a, width(1), groups(width(1)), ctas);
+  if (width(2) <= 384) return norm_bwd_launch<T, 2, kSum>(a, width(2), groups(width(2)), ctas);
+  if (width(4) <= 512) return norm_bwd_launch<T, 4, kSum>(a, width(4), 1, ctas);
+  return norm_bwd_launch<T, 0, kSum>(a, 512, 1, ctas);
 }
 
 template <typename T>
 moe_status norm_bwd_typed(const NormBwdArgs& a, void* dweight) {
-  const int nvec = a.d / moe::Vec16<T>::kN;
-  auto width = [&](int vpt) { return ((nvec + vpt - 1) / vpt + 31) / 32 * 32; };
-  if (a.T > 0) {
-    cudaError_t e;
-    if (width(1) <= 256) e = norm_bwd_launch<T, 1>(a, width(1));
-    else if (width(2) <= 256) e = norm_bwd_launch<T, 2>(a, width(2));
-    else if (width(4) <= 512) e = norm_bwd_launch<T, 4>(a, width(4));
-    else e = norm_bwd_launch<T, 0>(a, 512);
-    MOE_TRY(launched(e, "RMS norm backward"));
-  }
-  return launched(moe::launch_pdl(moe::rmsnorm_dw_kernel<T>, dim3((a.d + 31) / 32), dim3(256), 0,
-                                  a.st, a.part, a.T > 0 ? norm_bwd_ctas(a.T) : 0, a.d,
-                                  static_cast<T*>(dweight)),
+  int ctas = 0;
+  if (a.T > 0)
+    MOE_TRY(launched(a.dsum ? norm_bwd_dispatch<T, true>(a, &ctas)
+                            : norm_bwd_dispatch<T, false>(a, &ctas),
+                     "RMS norm backward"));
+  return launched(moe::launch_pdl(moe::rmsnorm_dw_kernel<T>, dim3((a.d + 31) / 32), dim3(1024), 0,
+                                  a.st, a.part, ctas, a.d, static_cast<T*>(dweight)),
                   "RMS norm weight gradient");
 }
 

@@ -164,11 +164,16 @@ rmsnorm_kernel(const T* x, const T* res, const T* __restrict__ w, float eps, int
   }
 }
 
-// Backward: CTA c takes rows c, c + grid, ...; its threads own the same columns
-// in every row, so dw accumulates in registers and the CTA writes one fp32
-// partial row.  The next row is loaded before the reduction of this one.
-// VPT = 0: rows longer than the registers hold; the partial row is kept in
-// global memory instead (each thread adds to its own columns).
+// Backward: the CTA's blockDim.y row groups take rows base + group, base advancing
+// by the grid; a thread owns the same columns in every row, so dw accumulates in
+// registers and a CTA writes one fp32 partial row.  A thread copies its own
+// vectors of s, dy and dsum into its own slots of a shared-memory ring kBwdDepth - 1
+// rows ahead (cp.async, no barrier: nobody else reads them), so the copies of the
+// next rows run under this row's reduction, which is the only block-wide wait.
+// VPT = 0: rows longer than the ring holds; they are read twice and the partial
+// row is kept in global memory (each thread adds to its own columns).
+constexpr int kBwdDepth = 3;
+
 template <typename T, int VPT, bool kSum>
 __global__ void __launch_bounds__(512)
 rmsnorm_bwd_kernel(const T* s, const T* __restrict__ w, const float* __restrict__ inv_rms,
@@ -176,71 +181,87 @@ rmsnorm_bwd_kernel(const T* s, const T* __restrict__ w, const float* __restrict_
   pdl_trigger();
   pdl_wait();
   constexpr int VN = Vec16<T>::kN;
-  __shared__ float red[2][32];
+  __shared__ float red[2][32 * 8];
   const int nvec = d / VN, tid = threadIdx.x, step = blockDim.x;
   const uint4* wv = reinterpret_cast<const uint4*>(w);
   float* mine = part + (size_t)blockIdx.x * d;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
   int flip = 0;
   if constexpr (VPT > 0) {
-    uint4 wr[VPT], sa[VPT], ya[VPT];
-    float dw[VPT][VN];
+    constexpr int kIn = kSum ? 3 : 2;
+    extern __shared__ uint4 ring[];  // [kBwdDepth][kIn][VPT][threads]
+    const int threads = blockDim.x * blockDim.y, me = threadIdx.y * blockDim.x + tid;
+    // unsigned: the fetch runs past a row count next to 2^31
+    const unsigned n_rows = rows, stride = gridDim.x * blockDim.y;
+    const unsigned first = blockIdx.x * blockDim.y + threadIdx.y;
+    auto slot = [&](int stage, int in, int i) -> uint4* {
+      return ring + (size_t)((stage * kIn + in) * VPT + i) * threads + me;
+    };
+    auto fetch = [&](unsigned r, int stage) {
+      if (r < n_rows) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = tid + i * step;
-      wr[i] = sa[i] = ya[i] = zero;
-      if (v < nvec) {
-        wr[i] = __ldg(wv + v);
-        if (blockIdx.x < rows) {
-          sa[i] = reinterpret_cast<const uint4*>(s + (size_t)blockIdx.x * d)[v];
-          ya[i] = reinterpret_cast<const uint4*>(dy + (size_t)blockIdx.x * d)[v];
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < VN; ++k) dw[i][k] = 0.f;
-    }
-    for (int r = blockIdx.x; r < rows; r += gridDim.x) {
-      uint4 cs[VPT], cy[VPT], add[VPT];
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int v = tid + i * step;
-        cs[i] = sa[i];
-        cy[i] = ya[i];
-        if (v < nvec) {
-          if constexpr (kSum) add[i] = reinterpret_cast<const uint4*>(dsum + (size_t)r * d)[v];
-          if (r + (int)gridDim.x < rows) {
-            const size_t nr = (size_t)(r + gridDim.x) * d;
-            sa[i] = reinterpret_cast<const uint4*>(s + nr)[v];
-            ya[i] = reinterpret_cast<const uint4*>(dy + nr)[v];
+        for (int i = 0; i < VPT; ++i) {
+          const int v = tid + i * step;
+          if (v < nvec) {
+            const size_t at = (size_t)r * d + (size_t)v * VN;
+            cp_async16(slot(stage, 0, i), s + at);
+            cp_async16(slot(stage, 1, i), dy + at);
+            if constexpr (kSum) cp_async16(slot(stage, 2, i), dsum + at);
           }
         }
       }
-      const float inv = inv_rms[r];
+      cp_async_commit();
+    };
+    uint4 wr[VPT];
+    float dw[VPT][VN];
+#pragma unroll
+    for (int k = 0; k < kBwdDepth - 1; ++k) fetch(first + k * stride, k);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = tid + i * step;
+      wr[i] = v < nvec ? __ldg(wv + v) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int k = 0; k < VN; ++k) dw[i][k] = 0.f;
+    }
+    int stage = 0;
+    // the loop runs by the CTA's first row: its groups keep step with one another
+    for (unsigned base = blockIdx.x * blockDim.y, r = first; base < n_rows;
+         base += stride, r += stride) {
+      const int ahead = stage ? stage - 1 : kBwdDepth - 1;  // the slots of the row before
+      fetch(r + (kBwdDepth - 1) * stride, ahead);
+      const bool live = r < n_rows;
+      const float inv = live ? inv_rms[r] : 0.f;
+      cp_async_wait<kBwdDepth - 1>();
+      uint4 cs[VPT], cy[VPT];
       float c = 0.f;
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
-        float f[VN], g[VN], ww[VN];
-        unpack16(cs[i], f, T());
-        unpack16(cy[i], g, T());
-        unpack16(wr[i], ww, T());
+        const int v = tid + i * step;
+        if (live && v < nvec) {
+          cs[i] = *slot(stage, 0, i);
+          cy[i] = *slot(stage, 1, i);
+          float f[VN], g[VN], ww[VN];
+          unpack16(cs[i], f, T());
+          unpack16(cy[i], g, T());
+          unpack16(wr[i], ww, T());
 #pragma unroll
-        for (int k = 0; k < VN; ++k) {
-          const float p = g[k] * (f[k] * inv);
-          c = fmaf(ww[k], p, c);
-          dw[i][k] += p;
+          for (int k = 0; k < VN; ++k) {
+            const float p = g[k] * (f[k] * inv);
+            c = fmaf(ww[k], p, c);
+            dw[i][k] += p;
+          }
         }
       }
-      c = row_sum(c, red[flip]) / (float)d;
+      c = row_sum(c, red[flip] + 32 * threadIdx.y) / (float)d;
       flip ^= 1;
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int v = tid + i * step;
-        if (v >= nvec) continue;
+        if (!live || v >= nvec) continue;
         float f[VN], g[VN], ww[VN], o[VN];
         unpack16(cs[i], f, T());
         unpack16(cy[i], g, T());
         unpack16(wr[i], ww, T());
-        if constexpr (kSum) unpack16(add[i], o, T());
+        if constexpr (kSum) unpack16(*slot(stage, 2, i), o, T());
 #pragma unroll
         for (int k = 0; k < VN; ++k) {
           const float t = inv * (ww[k] * g[k] - f[k] * inv * c);
@@ -248,6 +269,33 @@ rmsnorm_bwd_kernel(const T* s, const T* __restrict__ w, const float* __restrict_
         }
         reinterpret_cast<uint4*>(dx + (size_t)r * d)[v] = pack16(o, T());
       }
+      stage = stage + 1 == kBwdDepth ? 0 : stage + 1;
+    }
+    // one partial row a CTA: the groups' sums joined in group order
+    if (blockDim.y > 1) {
+      cp_async_wait<0>();
+      __syncthreads();
+      float4* all = reinterpret_cast<float4*>(ring);  // [group][VPT][VN / 4][blockDim.x]
+      constexpr int kQ = VN / 4;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int k = 0; k < kQ; ++k)
+          all[((threadIdx.y * VPT + i) * kQ + k) * step + tid] = make_float4(
+              dw[i][4 * k], dw[i][4 * k + 1], dw[i][4 * k + 2], dw[i][4 * k + 3]);
+      __syncthreads();
+      if (threadIdx.y > 0) return;
+      for (int y = 1; y < (int)blockDim.y; ++y)
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+#pragma unroll
+          for (int k = 0; k < kQ; ++k) {
+            const float4 o = all[((y * VPT + i) * kQ + k) * step + tid];
+            dw[i][4 * k] += o.x;
+            dw[i][4 * k + 1] += o.y;
+            dw[i][4 * k + 2] += o.z;
+            dw[i][4 * k + 3] += o.w;
+          }
     }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -299,25 +347,27 @@ rmsnorm_bwd_kernel(const T* s, const T* __restrict__ w, const float* __restrict_
   }
 }
 
-// dw[j] = sum over the n partial rows in a fixed order: 32 columns a CTA, 8
-// warps that each sum every eighth row, joined in warp order.  n = 0 gives 0.
+// dw[j] = sum over the n partial rows in a fixed order: 32 columns a CTA, 32
+// warps that each sum every 32nd row, joined in warp order.  n = 0 gives 0.
 template <typename T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(1024)
 rmsnorm_dw_kernel(const float* __restrict__ part, int n, int d, T* __restrict__ dw) {
   pdl_trigger();
   pdl_wait();
-  __shared__ float acc[8][32];
+  __shared__ float acc[32][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int j = blockIdx.x * 32 + lane;
   float v = 0.f;
-  if (j < d)
-    for (int r = warp; r < n; r += 8) v += part[(size_t)r * d + j];
+  if (j < d) {
+#pragma unroll 8
+    for (int r = warp; r < n; r += 32) v += part[(size_t)r * d + j];
+  }
   acc[warp][lane] = v;
   __syncthreads();
   if (warp == 0 && j < d) {
     float t = acc[0][lane];
 #pragma unroll
-    for (int k = 1; k < 8; ++k) t += acc[k][lane];
+    for (int k = 1; k < 32; ++k) t += acc[k][lane];
     dw[j] = Cvt<T>::from_f(t);
   }
 }
