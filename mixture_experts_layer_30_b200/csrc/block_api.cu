@@ -226,6 +226,18 @@ moe_status w4_simt(const moe_shape& s, const W4Args& a) {
       kGated ? "4-bit gate/up" : "4-bit down");
 }
 
+template <int GPS, bool kGated, int WR, int MaxNT>
+moe_status w4_launch(const moe::W4Problem& p, long long items, cudaStream_t st) {
+  auto* kernel = moe::w4_mma_kernel<GPS, kGated, WR, MaxNT>;
+  constexpr int smem = moe::W4Cfg<GPS, WR, MaxNT>::kBytes;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "4-bit product: %s", cudaGetErrorString(e));
+  const dim3 grid((unsigned)std::min(items, 2LL * sm_count()));
+  return launched(moe::launch_pdl(kernel, grid, dim3(moe::kW4Warps * 32), smem, st, p),
+                  kGated ? "4-bit gate/up" : "4-bit down");
+}
+
 template <int GPS, bool kGated>
 moe_status w4_mma(const moe_shape& s, const W4Args& a) {
   const moe::W4Problem p{{static_cast<const uint8_t*>(a.q0), static_cast<const uint8_t*>(a.q1)},
@@ -234,19 +246,16 @@ moe_status w4_mma(const moe_shape& s, const W4Args& a) {
                          static_cast<const __nv_bfloat16*>(a.a), a.a_rows, a.offsets, s.N,
                          s.T * s.K, s.T, a.n_out, a.k_dim, static_cast<__nv_bfloat16*>(a.c),
                          a.status};
-  const long long ctas = 2LL * sm_count();
   const long long rb = moe::w4_row_blocks(a.n_out), units = kGated ? rb : (rb + 1) / 2;
-  // At most one chunk per touched expert and 32 rows: with too few pairs of row
-  // blocks for every CTA to have some, a CTA takes one pair in eight slices.
   const long long max_rows = (long long)s.T * s.K;
-  const long long chunks = std::min<long long>(s.N, max_rows) + max_rows / moe::kW4MaxTokens;
-  const bool narrow = chunks * ((units + 1) / 2) < 2 * ctas;
-  const long long items = chunks * (narrow ? units : (units + 1) / 2);
-  const dim3 grid((unsigned)std::min(items, ctas));
-  return launched(moe::launch_pdl(narrow ? moe::w4_mma_kernel<GPS, kGated, 1>
-                                         : moe::w4_mma_kernel<GPS, kGated, 2>,
-                                  grid, dim3(moe::kW4Warps * 32), 0, a.st, p),
-                  kGated ? "4-bit gate/up" : "4-bit down");
+  // at most this many row chunks: one per expert that can have rows, one per full chunk
+  auto items = [&](int rows, int wr) {
+    return (std::min<long long>(s.N, max_rows) + max_rows / rows) * ((units + wr - 1) / wr);
+  };
+  // mean rows of an expert at most 4: one column tile holds nearly every expert's
+  if (max_rows <= 4LL * (s.N + s.Z))
+    return w4_launch<GPS, kGated, 2, 1>(p, items(8, 2), a.st);
+  return w4_launch<GPS, kGated, 8, 4>(p, items(32, 8), a.st);
 }
 
 template <bool kGated>
