@@ -229,7 +229,7 @@ moe_status w4_simt(const moe_shape& s, const W4Args& a) {
 template <int GPS, bool kGated, int WR, int MaxNT>
 moe_status w4_launch(const moe::W4Problem& p, long long items, cudaStream_t st) {
   auto* kernel = moe::w4_mma_kernel<GPS, kGated, WR, MaxNT>;
-  constexpr int smem = moe::W4Cfg<GPS, WR, MaxNT>::kBytes;
+  const int smem = moe::W4Cfg<GPS, WR, MaxNT>::kBytes + (2 * (p.N + 1) + 33) * (int)sizeof(int);
   const cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "4-bit product: %s", cudaGetErrorString(e));
@@ -255,7 +255,7 @@ moe_status w4_mma(const moe_shape& s, const W4Args& a) {
   // mean rows of an expert at most 4: one column tile holds nearly every expert's
   if (max_rows <= 4LL * (s.N + s.Z))
     return w4_launch<GPS, kGated, 2, 1>(p, items(8, 2), a.st);
-  return w4_launch<GPS, kGated, 8, 4>(p, items(32, 8), a.st);
+  return w4_launch<GPS, kGated, 4, 4>(p, items(32, 4), a.st);
 }
 
 template <bool kGated>

@@ -186,11 +186,13 @@ w4_simt_kernel(const T* __restrict__ A, const uint32_t* __restrict__ q0,
 //     four multiply-adds.  Products are exact in fp32; each group's fp32 sum is
 //     multiplied by the group's scale in fp32, so the weights are never rounded.
 //   * The CTA's eight warps take WR pairs of row blocks times WK = 8 / WR slices of
-//     the contraction; slices are joined through shared memory in slice order.
-//   * Items (row chunk of an expert, WR pairs of row blocks) are cut into equal
-//     contiguous runs, one per CTA.  Codes, scales and token rows come through a ring
-//     of shared-memory stages (cp.async), filled D - 1 steps ahead across items; a
-//     warp's codes are its own, a token tile is shared by the WR warps of a slice.
+//     the contraction; the warps of a pair join their slices through shared memory in
+//     slice order.
+//   * Items (row chunk of an expert, WR pairs of row blocks) are cut into contiguous
+//     runs of equal cost, one per CTA.  Codes and scales come through a ring of
+//     shared-memory stages (cp.async) filled two steps ahead across items, token rows
+//     (from L2) one step ahead; a warp's codes are its own, a token tile
+//     is shared by the WR warps of a slice.
 // ---------------------------------------------------------------------------
 constexpr int kW4Warps = 8;
 
@@ -255,45 +257,99 @@ struct W4Problem {
   uint32_t* status;
 };
 
-// Shared memory of one kernel variant.  NT: column tiles of 8 rows per chunk.
+// One kernel variant.  NT: column tiles of 8 rows per chunk.
 template <int GPS, int WR, int NT>
 struct W4Cfg {
+  static_assert(WR >= NT, "a warp copies pieces of one column tile");
   static constexpr int kWk = kW4Warps / WR, kRows = 8 * NT;
-  static constexpr int kDepth = NT == 1 ? 3 : 4;
+  static constexpr int kDepth = 3;
   static constexpr int kScaleBytes = 2 * kW4Rows * GPS * 2;     // of a warp's two row blocks
   static constexpr int kCodeStage = 2 * kW4Block + kScaleBytes;
   static constexpr int kXStage = NT * 4 * 512;
   static constexpr int kCodes = kW4Warps * kDepth * kCodeStage;
-  static constexpr int kX = kWk * kDepth * kXStage;
-  static constexpr int kRed = kWk > 1 ? kW4Warps * 2 * NT * 512 : 0;
-  static constexpr int kBytes = kCodes + kX + kRed;
+  static constexpr int kX = kWk * 2 * kXStage;
+  static constexpr int kRed = (kWk - 1) * WR * 2 * NT * 512;
+  static constexpr int kBytes = kCodes + kX + kRed;  // and two tables of N + 1 and 33 ints
+  // Cost of a chunk of nt column tiles: decoding the codes against their products, as the
+  // times of one to four tiles stand to one another.
+  static MOE_DEV int weight(int rows) { return 5 + 2 * ((rows + 7) / 8); }
 };
 
-// A position in a CTA's run of items: chunk of an expert's rows and group of WR
-// pairs of row blocks.
+// An item: WR pairs of row blocks (group) for one chunk of an expert's rows.
+template <typename Cfg>
 struct W4Cursor {
-  int e, chunk, group;
+  int e, c, group;
   int r0, rows;  // first routed row of the chunk and how many
-  MOE_DEV void rows_of(const W4Problem& p, const int* prefix, int per) {
-    r0 = p.offsets[e] + (chunk - prefix[e]) * per;
-    rows = min(per, (int)p.offsets[e + 1] - r0);
+  MOE_DEV void take(const int* off) {
+    r0 = off[e] + c * Cfg::kRows;
+    rows = min(Cfg::kRows, off[e + 1] - r0);
   }
-  MOE_DEV void set(const W4Problem& p, const int* prefix, int per, int c, int g) {
-    chunk = c;
-    group = g;
-    e = find_expert(prefix, p.N, c);
-    rows_of(p, prefix, per);
+  // Behind the expert's last chunk: to the next expert that has rows (or to N).
+  MOE_DEV void settle(const int* off, const int* cost, int N) {
+    if (off[e] + c * Cfg::kRows < off[e + 1]) return;
+    c = 0;
+    do ++e;
+    while (e < N && cost[e + 1] == cost[e]);
   }
-  // to the next item of the run; true: it is of another chunk
-  MOE_DEV bool next(const W4Problem& p, const int* prefix, int per, int groups) {
+  // The first item that starts at or behind `at` in the order of all costs.
+  MOE_DEV void seek(const int* off, const int* cost, int N, int groups, long long at) {
+    c = group = 0;
+    e = N;
+    if (at >= (long long)cost[N] * groups) return;
+    e = find_expert(cost, N, (int)(at / groups));
+    long long rem = at - (long long)cost[e] * groups;
+    const long long full = (long long)Cfg::weight(Cfg::kRows) * groups;
+    c = (int)min(rem / full, (long long)((off[e + 1] - off[e] - 1) / Cfg::kRows));
+    rem -= c * full;
+    take(off);
+    const int w = Cfg::weight(rows);
+    group = (int)((rem + w - 1) / w);
+    if (group >= groups) {
+      group = 0;
+      ++c;
+      settle(off, cost, N);
+    }
+  }
+  // To the next item; true: it is of another chunk.
+  MOE_DEV bool next(const int* off, const int* cost, int N, int groups) {
     if (++group < groups) return false;
     group = 0;
-    ++chunk;
-    while (e + 1 < p.N && prefix[e + 1] <= chunk) ++e;
-    rows_of(p, prefix, per);
+    ++c;
+    settle(off, cost, N);
     return true;
   }
+  MOE_DEV bool same(const W4Cursor& o) const { return e == o.e && c == o.c && group == o.group; }
 };
+
+// cost[e] = sum of the weights of experts 0..e-1's chunks, off[] = offsets; segments that
+// are not ascending or out of range count as empty and are reported.  Ends with a barrier.
+template <typename Cfg>
+MOE_DEV void w4_costs(const W4Problem& p, int* off, int* cost, int* scan_tmp) {
+  const int per = (p.N + blockDim.x - 1) / blockDim.x;
+  const int lo = min(p.N, (int)threadIdx.x * per), hi = min(p.N, lo + per);
+  auto weigh = [&](int e, bool report) {
+    const int a = p.offsets[e], b = p.offsets[e + 1], m = b - a;
+    if (report) off[e] = a;
+    if (m < 0 || a < 0 || b > p.max_rows) {
+      if (report) set_status(p.status, MOE_DEV_BAD_OFFSETS);
+      return 0;
+    }
+    const int full = m / Cfg::kRows, rest = m % Cfg::kRows;
+    return full * Cfg::weight(Cfg::kRows) + (rest ? Cfg::weight(rest) : 0);
+  };
+  int local = 0;
+  for (int e = lo; e < hi; ++e) local += weigh(e, true);
+  int run = block_exclusive_scan(local, scan_tmp, &scan_tmp[32]);
+  for (int e = lo; e < hi; ++e) {
+    cost[e] = run;
+    run += weigh(e, false);
+  }
+  if (threadIdx.x == 0) {
+    cost[p.N] = scan_tmp[32];
+    off[p.N] = p.offsets[p.N];
+  }
+  __syncthreads();
+}
 
 // One step's products of a warp's two row blocks with NT column tiles.
 template <int GPS, int NT>
@@ -344,14 +400,14 @@ MOE_DEV void w4_step(const char* codes, const char* xs, float (&acc)[2][NT][4]) 
 }
 
 // Stores one 16 x 8 piece of the result: output columns c0, c0 + 8 of rows i0, i0 + 1.
-MOE_DEV void w4_store(const W4Problem& p, const W4Cursor& it, int rb, int n, float4 v) {
+MOE_DEV void w4_store(const W4Problem& p, int r0, int rows, int rb, int n, float4 v) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int i0 = n * 8 + 2 * t, c0 = rb * kW4Rows + g;
-  __nv_bfloat16* out = p.c + (size_t)(it.r0 + i0) * p.n_out;
+  __nv_bfloat16* out = p.c + (size_t)(r0 + i0) * p.n_out;
   const float f[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int k = 0; k < 4; ++k)
-    if (i0 + (k & 1) < it.rows && c0 + (k >> 1) * 8 < p.n_out)
+    if (i0 + (k & 1) < rows && c0 + (k >> 1) * 8 < p.n_out)
       out[(size_t)(k & 1) * p.n_out + c0 + (k >> 1) * 8] = __float2bfloat16_rn(f[k]);
 }
 
@@ -365,99 +421,115 @@ MOE_DEV float4 w4_act(float4 v, float4 up) {
 template <int GPS, bool kGated, int WR, int MaxNT>
 struct W4Kernel {
   using Cfg = W4Cfg<GPS, WR, MaxNT>;
+  using Cursor = W4Cursor<Cfg>;
   static constexpr int WK = Cfg::kWk, D = Cfg::kDepth;
-  // token pieces (column tile, 32-column piece) that a warp copies per stage, and the
-  // column tiles among them
-  static constexpr int kPieces = MaxNT * 4 >= WR ? MaxNT * 4 / WR : 1;
-  static constexpr int kTiles = WR == 8 ? (MaxNT + 1) / 2 : MaxNT;
+  static constexpr int kPieces = 4 * MaxNT / WR;  // 32-column pieces a warp copies per token tile
+  static constexpr int kEach = GPS == 4 ? 8 : 4;  // bytes of scales a lane copies
+  static constexpr int kHalf = Cfg::kScaleBytes / 2 / kEach;  // lanes of one block's scales
 
   const W4Problem& p;
-  const int* prefix;
+  const int *off, *cost;
   char *codes, *xs;  // this warp's and this slice's ring
-  float4* red;
+  float4* red;       // this pair's
   int rb_n, sp_n, groups, n_steps, ks, wu;
-  W4Cursor load;
-  int load_step, load_slot, slot;
-  long long load_left;   // items of the run that are not loaded yet
-  int xrow[kTiles];
+  // codes: the next step to copy, its addresses
+  Cursor load;
+  int load_step, load_left, load_slot;
+  const uint8_t *qa, *qb;
+  const char* sc;
+  // token rows: the same, one step ahead of the products
+  Cursor xload;
+  int x_step, x_left, x_slot;
+  const __nv_bfloat16* xp;
+  int slot, x_read;  // the ring positions of the products
 
+  // A row block past the last repeats it; its results are not stored.
   MOE_DEV int row_block(int group, int m) const {
     const int u = group * WR + wu;
-    // a row block past the last repeats it; its results are not stored
     return min(kGated ? u : 2 * u + m, rb_n - 1);
   }
-  MOE_DEV int tile_of(int i) const { return WR == 8 ? 2 * i + (wu >> 2) : i; }
-
-  // The token rows that this lane copies of the load cursor's chunk.
-  MOE_DEV void take_rows() {
-    const int g = (threadIdx.x & 31) >> 2;
+  MOE_DEV void code_item() {
+    const int lane = threadIdx.x & 31;
+    long long blk[2];
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) {
-      const int r = tile_of(i) * 8 + g;
-      xrow[i] = 0;
-      if (r < load.rows) {
-        xrow[i] = load.r0 + r;
-        if (p.a_rows) {
-          xrow[i] = p.a_rows[load.r0 + r];
-          if (xrow[i] < 0 || xrow[i] >= p.a_src_rows) {
-            set_status(p.status, MOE_DEV_BAD_OFFSETS);
-            xrow[i] = 0;
-          }
-        }
-      }
-    }
+    for (int m = 0; m < 2; ++m)
+      blk[m] = ((long long)load.e * rb_n + row_block(load.group, m)) * sp_n + ks;
+    qa = p.q[0] + blk[0] * kW4Block + lane * 16;
+    qb = p.q[kGated ? 1 : 0] + blk[1] * kW4Block + lane * 16;
+    const int m = lane / kHalf & 1;
+    sc = reinterpret_cast<const char*>(m && kGated ? p.s[1] : p.s[0]) +
+         (m ? blk[1] : blk[0]) * (kW4Rows * GPS * 2) + (lane % kHalf) * kEach;
   }
-
-  // Issues the copies of the load cursor's step and moves it on; one group per call.
-  MOE_DEV void fill() {
+  MOE_DEV void fill_codes() {
     if (load_left > 0) {
-      const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-      const int kb = ks + load_step * WK;
+      const int lane = threadIdx.x & 31;
       char* dst = codes + load_slot * Cfg::kCodeStage;
-      long long blk[2];
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        blk[m] = ((long long)load.e * rb_n + row_block(load.group, m)) * sp_n + kb;
-        const uint8_t* q = p.q[kGated ? m : 0] + blk[m] * kW4Block + lane * 16;
-        cp_async16(dst + m * kW4Block + lane * 16, q);
-        cp_async16(dst + m * kW4Block + kW4Block / 2 + lane * 16, q + kW4Block / 2);
-      }
-      constexpr int kEach = GPS == 4 ? 8 : 4, kHalf = Cfg::kScaleBytes / 2 / kEach;  // lanes per block
-      if (lane < 2 * kHalf) {
-        const int m = lane / kHalf;
-        const char* s = reinterpret_cast<const char*>(p.s[kGated ? m : 0]) +
-                        (m ? blk[1] : blk[0]) * (kW4Rows * GPS * 2) + (lane % kHalf) * kEach;
-        cp_async_small<kEach>(dst + 2 * kW4Block + lane * kEach, s);
-      }
-      char* xd = xs + load_slot * Cfg::kXStage + lane * 16;
-#pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
-        const int piece = wu + i * WR, n = piece >> 2, j = piece & 3;
-        const int row = xrow[WR == 8 ? i : WR == 4 ? i : WR == 2 ? i / 2 : i / 4];
-        const int k = kb * kW4Cols + 32 * j + 8 * t;
-        if (piece < MaxNT * 4 && n * 8 + g < load.rows) {
-          if (k < p.k_dim) cp_async16(xd + piece * 512, p.a + (size_t)row * p.k_dim + k);
-          else *reinterpret_cast<uint4*>(xd + piece * 512) = make_uint4(0, 0, 0, 0);
-        }
-      }
+      cp_async16(dst + lane * 16, qa);
+      cp_async16(dst + kW4Block / 2 + lane * 16, qa + kW4Block / 2);
+      cp_async16(dst + kW4Block + lane * 16, qb);
+      cp_async16(dst + kW4Block + kW4Block / 2 + lane * 16, qb + kW4Block / 2);
+      if (lane < 2 * kHalf) cp_async_small<kEach>(dst + 2 * kW4Block + lane * kEach, sc);
+      qa += WK * kW4Block;
+      qb += WK * kW4Block;
+      sc += WK * kW4Rows * GPS * 2;
       load_slot = load_slot + 1 == D ? 0 : load_slot + 1;
       if (++load_step == n_steps) {
         load_step = 0;
-        if (--load_left > 0 && load.next(p, prefix, Cfg::kRows, groups)) take_rows();
+        if (--load_left > 0) {
+          load.next(off, cost, p.N, groups);
+          code_item();
+        }
       }
     }
     cp_async_commit();
   }
 
-  // The WR warps of a slice.
-  MOE_DEV void slice_sync() {
-    if constexpr (WR == 1) __syncwarp();
-    else asm volatile("bar.sync %0, %1;" ::"r"(1 + ks), "n"(WR * 32) : "memory");
+  // This lane's part of the chunk's token rows: row g of column tile wu / (WR / MaxNT), the
+  // pieces from wu % (WR / MaxNT) * kPieces on, eight columns t of each.
+  MOE_DEV void x_item() {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int r = wu / (WR / MaxNT) * 8 + g;
+    int row = 0;
+    if (r < xload.rows) {
+      row = xload.r0 + r;
+      if (p.a_rows) {
+        row = p.a_rows[row];
+        if (row < 0 || row >= p.a_src_rows) {
+          set_status(p.status, MOE_DEV_BAD_OFFSETS);
+          row = 0;
+        }
+      }
+    }
+    xp = p.a + (size_t)row * p.k_dim + ks * kW4Cols + wu % (WR / MaxNT) * kPieces * 32 + 8 * t;
+  }
+  MOE_DEV void fill_x() {
+    if (x_left > 0) {
+      const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+      const int tile = wu / (WR / MaxNT), piece = wu % (WR / MaxNT) * kPieces;
+      if (tile * 8 + g < xload.rows) {
+        char* dst = xs + x_slot * Cfg::kXStage + (tile * 4 + piece) * 512 + lane * 16;
+        const int k = (ks + x_step * WK) * kW4Cols + piece * 32 + 8 * t;
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+          if (k + 32 * j < p.k_dim) cp_async16(dst + j * 512, xp + x_step * WK * kW4Cols + 32 * j);
+          else *reinterpret_cast<uint4*>(dst + j * 512) = make_uint4(0, 0, 0, 0);
+        }
+      }
+      x_slot ^= 1;
+      if (++x_step == n_steps) {
+        x_step = 0;
+        if (--x_left > 0 && xload.next(off, cost, p.N, groups)) {
+          xload.take(off);
+          x_item();
+        }
+      }
+    }
+    cp_async_commit();
   }
 
   template <int NT>
-  MOE_DEV void item(const W4Cursor& it) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  MOE_DEV void item(const Cursor& it) {
+    const int lane = threadIdx.x & 31;
     float acc[2][NT][4];
 #pragma unroll
     for (int m = 0; m < 2; ++m)
@@ -466,52 +538,60 @@ struct W4Kernel {
 #pragma unroll
         for (int k = 0; k < 4; ++k) acc[m][n][k] = 0.f;
     for (int i = 0; i < n_steps; ++i) {
-      cp_async_wait<D - 2>();
-      slice_sync();  // every copy of this stage has landed, the stage before is read
-      fill();
-      w4_step<GPS, NT>(codes + slot * Cfg::kCodeStage, xs + slot * Cfg::kXStage, acc);
+      // all but the newest group, the next step's codes: it was issued behind this step's tokens
+      cp_async_wait<1>();
+      // every copy of this step has landed, and the step before is read
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + ks), "n"(WR * 32) : "memory");
+      fill_x();
+      fill_codes();
+      w4_step<GPS, NT>(codes + slot * Cfg::kCodeStage, xs + x_read * Cfg::kXStage, acc);
+      x_read ^= 1;
       slot = slot + 1 == D ? 0 : slot + 1;
     }
-    if constexpr (WK == 1) {
+    auto store = [&](int n, float4 v0, float4 v1) {
       const int u = it.group * WR + wu;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        if constexpr (kGated) {
-          if (u < rb_n) w4_store(p, it, u, n, w4_act(w4_scaled(acc[0][n]), w4_scaled(acc[1][n])));
-        } else {
-#pragma unroll
-          for (int m = 0; m < 2; ++m)
-            if (2 * u + m < rb_n) w4_store(p, it, 2 * u + m, n, w4_scaled(acc[m][n]));
-        }
+      if constexpr (kGated) {
+        if (u < rb_n) w4_store(p, it.r0, it.rows, u, n, w4_act(v0, v1));
+      } else {
+        if (2 * u < rb_n) w4_store(p, it.r0, it.rows, 2 * u, n, v0);
+        if (2 * u + 1 < rb_n) w4_store(p, it.r0, it.rows, 2 * u + 1, n, v1);
       }
+    };
+    if constexpr (WK == 1) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) store(n, w4_scaled(acc[0][n]), w4_scaled(acc[1][n]));
     } else {
-      // join the slices: slot (warp, row block, column tile) of 32 lanes
-      __syncthreads();  // the last item's sums have been read
+      // slices 1.. leave their sums to slice 0, which adds them in slice order
+      auto pair_sync = [&] {
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + WK + wu), "n"(WK * 32) : "memory");
+      };
+      pair_sync();  // the last item's sums have been read
+      if (ks > 0) {
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-          red[((warp * 2 + m) * NT + n) * 32 + lane] = w4_scaled(acc[m][n]);
-      __syncthreads();
-      constexpr int kOut = kGated ? WR * NT : WR * 2 * NT;  // 32-lane pieces of the result
-      for (int o = warp; o < kOut; o += kW4Warps) {
-        const int n = o % NT, m = kGated ? 0 : o / NT % 2, u = kGated ? o / NT : o / NT / 2;
-        auto join = [&](int mm) {
-          float4 v = red[((u * WK * 2 + mm) * NT + n) * 32 + lane];
+          for (int n = 0; n < NT; ++n)
+            red[(((ks - 1) * 2 + m) * NT + n) * 32 + lane] = w4_scaled(acc[m][n]);
+      }
+      pair_sync();
+      if (ks == 0) {
 #pragma unroll
-          for (int k = 1; k < WK; ++k) {
-            const float4 w = red[(((u * WK + k) * 2 + mm) * NT + n) * 32 + lane];
-            v.x += w.x;
-            v.y += w.y;
-            v.z += w.z;
-            v.w += w.w;
+        for (int n = 0; n < NT; ++n) {
+          float4 v[2];
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            v[m] = w4_scaled(acc[m][n]);
+#pragma unroll
+            for (int k = 0; k < WK - 1; ++k) {
+              const float4 w = red[((k * 2 + m) * NT + n) * 32 + lane];
+              v[m].x += w.x;
+              v[m].y += w.y;
+              v[m].z += w.z;
+              v[m].w += w.w;
+            }
           }
-          return v;
-        };
-        float4 v = join(m);
-        if (kGated) v = w4_act(v, join(1));
-        const int rb = kGated ? it.group * WR + u : 2 * (it.group * WR + u) + m;
-        if (rb < rb_n) w4_store(p, it, rb, n, v);
+          store(n, v[0], v[1]);
+        }
       }
     }
   }
@@ -525,43 +605,48 @@ w4_mma_kernel(const __grid_constant__ W4Problem p) {
   using K = W4Kernel<GPS, kGated, WR, MaxNT>;
   using Cfg = typename K::Cfg;
   constexpr int WK = Cfg::kWk;
-  __shared__ int prefix[kMaxExperts + 1];
-  __shared__ int scan_tmp[33];
   extern __shared__ __align__(16) char w4_smem[];
-  build_chunk_prefix(p.offsets, p.N, p.max_rows, Cfg::kRows, prefix, scan_tmp, p.status);
+  int* off = reinterpret_cast<int*>(w4_smem + Cfg::kBytes);
+  int* cost = off + p.N + 1;
+  w4_costs<Cfg>(p, off, cost, cost + p.N + 1);
   const int rb_n = w4_row_blocks(p.n_out), sp_n = w4_col_blocks(p.k_dim);
   const int units = kGated ? rb_n : (rb_n + 1) / 2;
   const int groups = (units + WR - 1) / WR;
-  const long long total = (long long)prefix[p.N] * groups;
-  const long long first = total * blockIdx.x / gridDim.x;
-  const long long end = total * (blockIdx.x + 1) / gridDim.x;
-  if (first >= end) return;
-  const int warp = threadIdx.x >> 5, ks = warp % WK;
-  K k{p, prefix, w4_smem + warp * Cfg::kDepth * Cfg::kCodeStage,
-      w4_smem + Cfg::kCodes + ks * Cfg::kDepth * Cfg::kXStage,
-      reinterpret_cast<float4*>(w4_smem + Cfg::kCodes + Cfg::kX)};
+  const long long total = (long long)cost[p.N] * groups;
+  typename K::Cursor cur, end;
+  cur.seek(off, cost, p.N, groups, total * blockIdx.x / gridDim.x);
+  end.seek(off, cost, p.N, groups, total * (blockIdx.x + 1) / gridDim.x);
+  int left = 0;
+  for (typename K::Cursor c = cur; !c.same(end); ++left) c.next(off, cost, p.N, groups);
+  if (left == 0) return;
+  cur.take(off);
+  const int warp = threadIdx.x >> 5, ks = warp % WK, wu = warp / WK;
+  K k{p, off, cost, w4_smem + warp * Cfg::kDepth * Cfg::kCodeStage,
+      w4_smem + Cfg::kCodes + ks * 2 * Cfg::kXStage,
+      reinterpret_cast<float4*>(w4_smem + Cfg::kCodes + Cfg::kX + wu * (Cfg::kRed / WR))};
   k.rb_n = rb_n;
   k.sp_n = sp_n;
   k.groups = groups;
   k.ks = ks;
-  k.wu = warp / WK;
+  k.wu = wu;
   k.n_steps = sp_n > ks ? (sp_n - ks + WK - 1) / WK : 0;
-  W4Cursor cur;
-  cur.set(p, prefix, Cfg::kRows, (int)(first / groups), (int)(first % groups));
-  k.load = cur;
-  k.load_step = k.load_slot = k.slot = 0;
-  k.load_left = k.n_steps > 0 ? end - first : 0;
-  k.take_rows();
+  k.load = k.xload = cur;
+  k.load_step = k.load_slot = k.x_step = k.x_slot = k.slot = k.x_read = 0;
+  k.load_left = k.x_left = k.n_steps > 0 ? left : 0;
+  k.code_item();
 #pragma unroll
-  for (int i = 0; i < Cfg::kDepth - 1; ++i) k.fill();
-  for (long long i = first;;) {
+  for (int i = 0; i < Cfg::kDepth - 2; ++i) k.fill_codes();
+  k.x_item();
+  k.fill_x();
+  k.fill_codes();
+  for (;;) {
     const int nt = (cur.rows + 7) / 8;
     if (MaxNT == 1 || nt <= 1) k.template item<1>(cur);
     else if (MaxNT >= 2 && nt == 2) k.template item<MaxNT >= 2 ? 2 : 1>(cur);
     else if (MaxNT >= 3 && nt == 3) k.template item<MaxNT >= 3 ? 3 : 1>(cur);
     else if (MaxNT >= 4) k.template item<MaxNT >= 4 ? 4 : 1>(cur);
-    if (++i >= end) break;
-    cur.next(p, prefix, Cfg::kRows, groups);
+    if (--left == 0) break;
+    if (cur.next(off, cost, p.N, groups)) cur.take(off);
   }
 }
 
