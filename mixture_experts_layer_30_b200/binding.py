@@ -156,7 +156,19 @@ def _p(t, dtype=None, name="tensor"):
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
+
+
+def _at(t, dtype, dev, name):
+    """_p of a tensor that has to lie on device `dev`, where the call launches.  (One
+    test of the three properties: the checks of a small call cost more than its kernel.)"""
+    if t is None:
+        return None
+    if t.get_device() == dev and t.dtype is dtype and t.is_contiguous():
+        return t.data_ptr()
+    p = _p(t, dtype, name)
+    _here(t)
+    return p
 
 
 _DTYPE_CODES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
@@ -179,9 +191,10 @@ def _rows(x):
 
 
 def _same(x, named):
+    shape = x.shape
     for name, t in named:
-        if t is not None and t.shape != x.shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(x.shape)}")
+        if t is not None and t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
 def _size(t, n, name):
@@ -190,8 +203,11 @@ def _size(t, n, name):
 
 
 def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    """Handle of `stream` or of torch's current stream (read directly: building a
+    torch.cuda.Stream for it takes longer than a launch)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def quantize_weights_mxfp8(w: torch.Tensor, stream=None):
@@ -276,17 +292,18 @@ def forward_mxfp8(buf: "LayerBuffers", fb: Mxfp8Buffers, x, w_router, w1, w3, w2
 def permute_mxfp8_rows(shape, x_q, x_sf, topk_idx, counts, offsets, row_token, slot_pos, x_perm_q,
                        x_perm_sf, ws, stream=None):
     """permute_mxfp8 for tokens held in MXFP8 already (rmsnorm's y_q, y_sf)."""
-    _here(x_q, x_sf, x_perm_q, x_perm_sf, ws)
-    _check(lib().moe_permute_mxfp8_rows(ctypes.byref(shape), _p(x_q, torch.uint8, "x_q"),
-                                        _p(x_sf, torch.uint8, "x_sf"),
-                                        _p(topk_idx, torch.int32, "topk_idx"),
-                                        _p(counts, torch.int32, "counts"),
-                                        _p(offsets, torch.int32, "offsets"),
-                                        _p(row_token, torch.int32, "row_token"),
-                                        _p(slot_pos, torch.int32, "slot_pos"),
-                                        _p(x_perm_q, torch.uint8, "x_perm_q"),
-                                        _p(x_perm_sf, torch.uint8, "x_perm_sf"), _p(ws),
-                                        ws.numel(), _stream(stream)))
+    dev = torch.cuda.current_device()
+    u8, i32 = torch.uint8, torch.int32
+    _check(lib().moe_permute_mxfp8_rows(ctypes.byref(shape), _at(x_q, u8, dev, "x_q"),
+                                        _at(x_sf, u8, dev, "x_sf"),
+                                        _at(topk_idx, i32, dev, "topk_idx"),
+                                        _at(counts, i32, dev, "counts"),
+                                        _at(offsets, i32, dev, "offsets"),
+                                        _at(row_token, i32, dev, "row_token"),
+                                        _at(slot_pos, i32, dev, "slot_pos"),
+                                        _at(x_perm_q, u8, dev, "x_perm_q"),
+                                        _at(x_perm_sf, u8, dev, "x_perm_sf"),
+                                        _at(ws, u8, dev, "ws"), ws.numel(), _stream(stream)))
 
 
 # ---------------------------------------------------------------------------
@@ -313,36 +330,37 @@ def quantize_weights_w4(w: torch.Tensor, group: int = 128, stream=None):
     return q, sc
 
 
-def _w4(pair, n, rows, cols, group, name):
+def _w4(pair, n, rows, cols, group, name, dev=None):
     """Pointers of a (codes, scales) pair whose sizes are checked."""
     q, sc = pair
     blocks = n * -(-rows // 16) * -(-cols // 128)
     if q.numel() != blocks * 1024 or sc.numel() != blocks * 2048 // group:
         raise ValueError(f"{name}: codes of {q.numel()} and scales of {sc.numel()} values do not "
                          f"hold {n} matrices [{rows}, {cols}] in groups of {group}")
-    return _p(q, torch.uint8, name), _p(sc, torch.bfloat16, name)
+    return _at(q, torch.uint8, dev, name), _at(sc, torch.bfloat16, dev, name)
 
 
 def expert_gate_up_w4(shape, group, x, row_token, w1, w3, offsets, h, ws, stream=None):
     """w1, w3: (codes, scales) pairs from quantize_weights_w4; row_token None: x is
     x_perm."""
-    dt = torch_dtype(shape)
-    _here(x, w1[0], w3[0], offsets, h, ws)
-    q1, s1 = _w4(w1, shape.N, shape.I, shape.d, group, "w1")
-    q3, s3 = _w4(w3, shape.N, shape.I, shape.d, group, "w3")
-    _check(lib().moe_expert_gate_up_w4(ctypes.byref(shape), group, _p(x, dt, "x"),
-                                       _p(row_token, torch.int32, "row_token"), q1, s1, q3, s3,
-                                       _p(offsets, torch.int32, "offsets"), _p(h, dt, "h"),
-                                       _p(ws), ws.numel(), _stream(stream)))
+    dt, dev = torch_dtype(shape), torch.cuda.current_device()
+    N, I, d = shape.N, shape.I, shape.d
+    q1, s1 = _w4(w1, N, I, d, group, "w1", dev)
+    q3, s3 = _w4(w3, N, I, d, group, "w3", dev)
+    _check(lib().moe_expert_gate_up_w4(ctypes.byref(shape), group, _at(x, dt, dev, "x"),
+                                       _at(row_token, torch.int32, dev, "row_token"), q1, s1, q3,
+                                       s3, _at(offsets, torch.int32, dev, "offsets"),
+                                       _at(h, dt, dev, "h"), _at(ws, torch.uint8, dev, "ws"),
+                                       ws.numel(), _stream(stream)))
 
 
 def expert_down_w4(shape, group, h, w2, offsets, y_perm, ws, stream=None):
-    dt = torch_dtype(shape)
-    _here(h, w2[0], offsets, y_perm, ws)
-    q2, s2 = _w4(w2, shape.N, shape.d, shape.I, group, "w2")
-    _check(lib().moe_expert_down_w4(ctypes.byref(shape), group, _p(h, dt, "h"), q2, s2,
-                                    _p(offsets, torch.int32, "offsets"),
-                                    _p(y_perm, dt, "y_perm"), _p(ws), ws.numel(),
+    dt, dev = torch_dtype(shape), torch.cuda.current_device()
+    q2, s2 = _w4(w2, shape.N, shape.d, shape.I, group, "w2", dev)
+    _check(lib().moe_expert_down_w4(ctypes.byref(shape), group, _at(h, dt, dev, "h"), q2, s2,
+                                    _at(offsets, torch.int32, dev, "offsets"),
+                                    _at(y_perm, dt, dev, "y_perm"),
+                                    _at(ws, torch.uint8, dev, "ws"), ws.numel(),
                                     _stream(stream)))
 
 
@@ -372,18 +390,17 @@ def rmsnorm(x, weight, eps, y, residual=None, sum_out=None, inv_rms=None, y_q=No
     inv_rms the row factors, y_q and y_sf the rounded y in MXFP8.  y may be None
     when y_q is given."""
     T, d, code = _rows(x)
-    dt = x.dtype
-    _here(x, weight, y, residual, sum_out, inv_rms, y_q, y_sf)
+    dt, dev, f32, u8 = x.dtype, torch.cuda.current_device(), torch.float32, torch.uint8
     _same(x, (("residual", residual), ("sum_out", sum_out), ("y", y)))
     _size(weight, d, "weight")
     _size(inv_rms, T, "inv_rms")
     _size(y_q, T * d, "y_q")
     _size(y_sf, T * (d // 32), "y_sf")
-    _check(lib().moe_rmsnorm(T, d, code, _p(x, dt, "x"), _p(residual, dt, "residual"),
-                             _p(weight, dt, "weight"), eps, _p(sum_out, dt, "sum_out"),
-                             _p(y, dt, "y"), _p(inv_rms, torch.float32, "inv_rms"),
-                             _p(y_q, torch.uint8, "y_q"), _p(y_sf, torch.uint8, "y_sf"),
-                             _stream(stream)))
+    _check(lib().moe_rmsnorm(T, d, code, _at(x, dt, dev, "x"), _at(residual, dt, dev, "residual"),
+                             _at(weight, dt, dev, "weight"), eps,
+                             _at(sum_out, dt, dev, "sum_out"), _at(y, dt, dev, "y"),
+                             _at(inv_rms, f32, dev, "inv_rms"), _at(y_q, u8, dev, "y_q"),
+                             _at(y_sf, u8, dev, "y_sf"), _stream(stream)))
 
 
 def new_rmsnorm_workspace(T: int, d: int, device="cuda") -> torch.Tensor:
@@ -397,16 +414,17 @@ def rmsnorm_backward(s, weight, inv_rms, dy, dx, dweight, ws, dsum=None, stream=
     """Gradients of rmsnorm: s is its sum_out (x without a residual), dsum the
     gradient along the residual stream; dx is the gradient of x and of residual."""
     T, d, code = _rows(s)
-    dt = s.dtype
-    _here(s, weight, inv_rms, dy, dx, dweight, ws, dsum)
+    dt, dev = s.dtype, torch.cuda.current_device()
     _same(s, (("dy", dy), ("dx", dx), ("dsum", dsum)))
     _size(weight, d, "weight")
     _size(dweight, d, "dweight")
     _size(inv_rms, T, "inv_rms")
-    _check(lib().moe_rmsnorm_backward(T, d, code, _p(s, dt, "s"), _p(weight, dt, "weight"),
-                                      _p(inv_rms, torch.float32, "inv_rms"), _p(dy, dt, "dy"),
-                                      _p(dsum, dt, "dsum"), _p(dx, dt, "dx"),
-                                      _p(dweight, dt, "dweight"), _p(ws), ws.numel(),
+    _check(lib().moe_rmsnorm_backward(T, d, code, _at(s, dt, dev, "s"),
+                                      _at(weight, dt, dev, "weight"),
+                                      _at(inv_rms, torch.float32, dev, "inv_rms"),
+                                      _at(dy, dt, dev, "dy"), _at(dsum, dt, dev, "dsum"),
+                                      _at(dx, dt, dev, "dx"), _at(dweight, dt, dev, "dweight"),
+                                      _at(ws, torch.uint8, dev, "ws"), ws.numel(),
                                       _stream(stream)))
 
 
@@ -505,21 +523,27 @@ class GradientList:
             wrote = max(wrote, b) if write else wrote
 
 
+def _norm_args(grads, norm):
+    dev = torch.cuda.current_device()
+    _size(norm, 1, "norm")
+    return (len(grads.tensors), grads.table, _at(norm, torch.float32, dev, "norm"),
+            _at(grads.ws, torch.uint8, dev, "grads.ws"))
+
+
 def gradient_norm(grads: GradientList, norm, stream=None):
     """norm[0] = the 2-norm of all gradients together (fp32, on the device)."""
-    _here(grads.ws, norm)
-    _size(norm, 1, "norm")
-    _check(lib().moe_grad_norm(len(grads.tensors), grads.table, _p(norm, torch.float32, "norm"),
-                               _p(grads.ws), grads.ws.numel(), _stream(stream)))
+    n, table, np, ws = _norm_args(grads, norm)
+    _check(lib().moe_grad_norm(n, table, np, ws, grads.ws.numel(), _stream(stream)))
     return norm
 
 
 def clip_gradients(grads: GradientList, max_norm, norm, stream=None):
     """Scales the gradients by min(1, max_norm / (norm + 1e-6)) into grads.out, with
     their global norm, which is left in norm[0]."""
-    gradient_norm(grads, norm, stream=stream)
-    _check(lib().moe_grad_clip(len(grads.tensors), grads.table, float(max_norm),
-                               _p(norm, torch.float32, "norm"), _stream(stream)))
+    n, table, np, ws = _norm_args(grads, norm)
+    st, L = _stream(stream), lib()
+    _check(L.moe_grad_norm(n, table, np, ws, grads.ws.numel(), st))
+    _check(L.moe_grad_clip(n, table, float(max_norm), np, st))
     return norm
 
 

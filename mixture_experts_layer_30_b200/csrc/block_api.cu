@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -64,11 +65,36 @@ moe_status optional(const void* p, const char* name, size_t align) {
 
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
+constexpr int kMaxDevices = 64;
+int current_device() {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices ? dev : -1;
+}
+
+// SMs of the current device, asked for once per device.
 int sm_count() {
-  int dev = 0, n = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess)
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n > 0 ? n : 148;
+  static std::atomic<int> known[kMaxDevices];
+  const int dev = current_device();
+  int n = dev >= 0 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (n > 0) return n;
+  if (dev < 0 ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+    return 148;
+  known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// Lets a kernel take up to `most` bytes of dynamic shared memory: set once per device (one
+// value for every call, so that calls of several threads cannot undo one another's).
+template <auto* kKernel>
+cudaError_t allow_smem(int most) {
+  static std::atomic<bool> done[kMaxDevices];
+  const int dev = current_device();
+  if (dev >= 0 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  if (e == cudaSuccess && dev >= 0) done[dev].store(true, std::memory_order_release);
+  return e;
 }
 
 moe_status need_ws(void* ws, size_t have, size_t want) {
@@ -153,11 +179,8 @@ cudaError_t norm_bwd_launch(const NormBwdArgs& a, int threads, int groups, int* 
   const int fit = smem ? (224 * 1024) / (smem + 2048) : 4;
   const int per_sm = std::max(1, std::min({4, fit, 1024 / (threads * groups)}));
   *ctas = std::min((a.T + groups - 1) / groups, std::min(sm_count() * per_sm, kNormBwdCtas));
-  if (smem + 2048 > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t e = allow_smem<moe::rmsnorm_bwd_kernel<T, VPT, kSum>>(222 * 1024);
+  if (e != cudaSuccess) return e;
   return moe::launch_pdl(kernel, dim3(*ctas), dim3(threads, groups), smem, a.st,
                          static_cast<const T*>(a.s), static_cast<const T*>(a.w), a.inv,
                          static_cast<const T*>(a.dy), static_cast<const T*>(a.dsum), a.T, a.d,
@@ -229,9 +252,11 @@ moe_status w4_simt(const moe_shape& s, const W4Args& a) {
 template <int GPS, bool kGated, int WR, int MaxNT>
 moe_status w4_launch(const moe::W4Problem& p, long long items, cudaStream_t st) {
   auto* kernel = moe::w4_mma_kernel<GPS, kGated, WR, MaxNT>;
-  const int smem = moe::W4Cfg<GPS, WR, MaxNT>::kBytes + (2 * (p.N + 1) + 33) * (int)sizeof(int);
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  constexpr int fixed = moe::W4Cfg<GPS, WR, MaxNT>::kBytes;
+  auto table = [](int n) { return (2 * (n + 1) + 33) * (int)sizeof(int); };
+  const int smem = fixed + table(p.N);
+  const cudaError_t e = allow_smem<moe::w4_mma_kernel<GPS, kGated, WR, MaxNT>>(
+      fixed + table(moe::kMaxExperts));
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "4-bit product: %s", cudaGetErrorString(e));
   const dim3 grid((unsigned)std::min(items, 2LL * sm_count()));
   return launched(moe::launch_pdl(kernel, grid, dim3(moe::kW4Warps * 32), smem, st, p),

@@ -187,8 +187,9 @@ grad_clip_kernel(const __grid_constant__ ClipTable tab, float max_norm, bool in_
   float coef = max_norm / (*norm + 1e-6f);
   if (coef > 1.0f) coef = 1.0f;  // NaN stays NaN
   if (in_place && coef == 1.0f) return;
+  // from the last chunk back: what the norm read last is still in L2
   const long long chunks = tab.first[tab.n];
-  for (long long c = blockIdx.x; c < chunks; c += gridDim.x) {
+  for (long long c = chunks - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
     const int i = clip_find(tab, c);
     const long long k = c - tab.first[i];
     if (tab.bf16[i >> 5] >> (i & 31) & 1)

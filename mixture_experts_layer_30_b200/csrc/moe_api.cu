@@ -224,9 +224,10 @@ cudaLaunchConfig_t cluster_config(dim3 grid, dim3 block, dim3 cluster, cudaStrea
 
 template <typename... KArgs, typename... Args>
 cudaError_t launch_cluster_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, dim3 cluster,
-                               cudaStream_t st, Args... args) {
+                               size_t smem, cudaStream_t st, Args... args) {
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = cluster_config(grid, block, cluster, st, attr);
+  cfg.dynamicSmemBytes = smem;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
@@ -282,7 +283,7 @@ void launch_small(const moe_shape& s, const SmallRoute& r, cudaStream_t st, cons
   // one cluster per token group when every group does not fit one resident cluster
   if (!cluster_size_ok(kernel, cluster)) cluster.y = 1;
   launch_cluster_pdl(kernel, dim3((unsigned)r.CL, (unsigned)small_clusters(s)),
-                     dim3(moe::kSmallThreads), cluster, st, static_cast<const T*>(x),
+                     dim3(moe::kSmallThreads), cluster, 0, st, static_cast<const T*>(x),
                      static_cast<const T*>(w), off, bias, s.T, s.d, E, s.N, s.K, idx, gate, nffn,
                      probs, hist, psum, ticket, counts, prob_sum, lay.offsets, lay.row_token,
                      lay.slot_pos);
@@ -459,6 +460,33 @@ moe_status permute_impl(const moe_shape& s, const void* x, const int32_t* idx,
     }
   }
   return MOE_OK;
+}
+
+// permute_impl without a copy, in one launch where the batch fits one cluster (and is
+// more than the one chunk that permute_impl takes in one launch itself).
+moe_status permute_layout(const moe_shape& s, const int32_t* idx, const int32_t* counts,
+                          int32_t* offsets, int32_t* row_token, int32_t* slot_pos, void* ws,
+                          const WsLayout& L, cudaStream_t st) {
+  if (perm_chunks(s) < 2 || s.T > moe::kPermClusterTokens)
+    return permute_impl<__nv_bfloat16>(s, nullptr, idx, counts, offsets, row_token, slot_pos,
+                                       nullptr, ws, L, st);
+  const int per = ((s.T + moe::kPermCluster - 1) / moe::kPermCluster + 31) / 32 * 32;
+  const size_t smem = moe::perm_cluster_smem(per, s.N);
+  if (smem > 40 * 1024) {
+    // one value for every call: the largest batch with the most experts
+    const cudaError_t e = cudaFuncSetAttribute(
+        moe::perm_cluster_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        (int)moe::perm_cluster_smem(moe::kPermClusterTokens / moe::kPermCluster, moe::kMaxExperts));
+    if (e != cudaSuccess)
+      return fail(MOE_ERR_CUDA, "dispatch layout: %s", cudaGetErrorString(e));
+  }
+  // one cluster per 64 of a CTA's tokens, 16 at most: 128 SMs
+  const int shares = std::max(1, std::min(16, per / 64));
+  const int threads = std::max(256, std::min(1024, per * s.K / 4 / 32 * 32));
+  launch_cluster_pdl(moe::perm_cluster_kernel, dim3(moe::kPermCluster * shares), dim3(threads),
+                     dim3(moe::kPermCluster), smem, st, idx, s.T, s.K, s.N, s.N + s.Z, per, counts,
+                     offsets, row_token, slot_pos, at<uint32_t>(ws, L.status));
+  return check_launch("dispatch layout");
 }
 
 template <typename T, bool kGated>
@@ -883,8 +911,7 @@ moe_status moe_permute_mxfp8_rows(const moe_shape* shape, const void* x_q, const
     MOE_TRY(need(x_perm_sf, "x_perm_sf", 16));
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  MOE_TRY(permute_impl<__nv_bfloat16>(s, nullptr, topk_idx, counts, offsets, row_token, slot_pos,
-                                      nullptr, ws, L, st));
+  MOE_TRY(permute_layout(s, topk_idx, counts, offsets, row_token, slot_pos, ws, L, st));
   if (s.T > 0) {
     const long long items = (long long)s.T * ((s.d + moe::kRowPiece - 1) / moe::kRowPiece + 1);
     if ((items + 7) / 8 > 0x7fffffffLL)

@@ -10,7 +10,8 @@
 //   3. rank_kernel        per chunk: row of (t, k) = base[c][e] + #earlier tokens of
 //                         the chunk routed to e (warp bitmaps + popcount)
 //   4. gather_kernel      one warp per token: x row copied to each of its rows.
-// A batch of one chunk (decode) runs 1-4 as one kernel (perm_gather_small_kernel),
+// The dispatch of 8-bit rows runs 1-3 of a batch of up to 8192 tokens as one kernel of
+// one cluster (perm_cluster_kernel).  A batch of one chunk (decode) runs 1-4 as one kernel (perm_gather_small_kernel),
 // or 1-3 as perm_small_kernel when no copy is asked for.
 #pragma once
 
@@ -185,6 +186,121 @@ perm_small_kernel(const int32_t* __restrict__ topk_idx, int T, int K, int N, int
       slot_pos[(size_t)t * K + k] = row;
     }
   }
+}
+
+// Histogram, scan and rank of a batch of up to kPermClusterTokens tokens in one launch.
+// A cluster of eight CTAs covers the batch: CTA r takes tokens r * per .. of `per` (a
+// multiple of 32), builds the bitmaps of their choices and reads the other CTAs'
+// histograms from their shared memory.  Every cluster does this for the whole batch,
+// without waiting for another, and ranks its share of each CTA's tokens (the stores of
+// row_token are scattered: one SM takes few of them at a time).  A token's experts are
+// distinct.
+// Shared: bits[W][N], hist[N], base[N], wbase[W][N] in 16 bits; W = per / 32.
+constexpr int kPermCluster = 8, kPermClusterTokens = 8 * 1024;
+inline size_t perm_cluster_smem(int per, int N) {
+  return (size_t)N * ((size_t)(per / 32) * 6 + 8);
+}
+
+MOE_DEV uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// The int at the address that `p` has in CTA `rank` of the cluster.
+MOE_DEV int cluster_load(const int* p, uint32_t rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;"
+      : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+static __global__ void __launch_bounds__(1024)
+perm_cluster_kernel(const int32_t* __restrict__ topk_idx, int T, int K, int N, int E, int per,
+                    const int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
+                    int32_t* __restrict__ row_token, int32_t* __restrict__ slot_pos,
+                    uint32_t* status) {
+  pdl_trigger();
+  pdl_wait();
+  extern __shared__ uint32_t sh_pc[];
+  __shared__ int scan_tmp[33];
+  const int W = per / 32;
+  uint32_t* bits = sh_pc;                                      // [W][N]
+  int* hist = reinterpret_cast<int*>(bits + (size_t)W * N);    // [N] rows of this CTA's tokens
+  int* base = hist + N;                                        // [N] first row of them
+  uint16_t* wbase = reinterpret_cast<uint16_t*>(base + N);     // [W][N] within the CTA
+  const uint32_t rank = cluster_rank();
+  const int share = blockIdx.x / kPermCluster, shares = gridDim.x / kPermCluster;
+  const bool writer = rank == 0 && share == 0;
+  const int t0 = (int)rank * per, nt = max(0, min(per, T - t0));
+  const int32_t* idx = topk_idx + (size_t)t0 * K;
+  for (int i = threadIdx.x; i < W * N; i += blockDim.x) bits[i] = 0;
+  __syncthreads();
+#pragma unroll 4
+  for (int i = threadIdx.x; i < nt * K; i += blockDim.x) {
+    const int e = __ldg(idx + i), t = i / K;
+    if (e < 0 || e >= E) {
+      if (share == 0) set_status(status, MOE_DEV_BAD_EXPERT_INDEX);
+    } else if (e < N) {
+      atomicOr(&bits[(t >> 5) * N + e], 1u << (t & 31));
+    }
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < N; e += blockDim.x) {
+    int c = 0;
+    for (int w = 0; w < W; ++w) {
+      wbase[w * N + e] = (uint16_t)c;
+      c += __popc(bits[w * N + e]);
+    }
+    hist[e] = c;
+  }
+  __syncwarp();
+  cluster_arrive();
+  cluster_wait();
+  // each thread owns a run of consecutive experts: totals, then their exclusive scan
+  const int run_len = (N + blockDim.x - 1) / blockDim.x;
+  const int lo = min(N, (int)threadIdx.x * run_len), hi = min(N, lo + run_len);
+  int local = 0;
+  for (int e = lo; e < hi; ++e) {
+    int before = 0, total = 0;
+#pragma unroll
+    for (int r = 0; r < kPermCluster; ++r) {
+      const int v = cluster_load(hist + e, r);
+      if (r < (int)rank) before += v;
+      total += v;
+    }
+    base[e] = before;
+    if (writer && counts && counts[e] != total) set_status(status, MOE_DEV_COUNT_MISMATCH);
+    local += total;
+  }
+  int run = block_exclusive_scan(local, scan_tmp, &scan_tmp[32]);
+  for (int e = lo; e < hi; ++e) {
+    if (writer) offsets[e] = run;
+    base[e] += run;
+    if (run_len > 1) {
+#pragma unroll
+      for (int r = 0; r < kPermCluster; ++r) run += cluster_load(hist + e, r);
+    }
+  }
+  __syncwarp();
+  if (writer && threadIdx.x == 0) offsets[N] = scan_tmp[32];
+  cluster_arrive();  // this CTA has read the others' histograms
+  __syncthreads();
+  const int first = min(nt, W * share / shares * 32), end = min(nt, W * (share + 1) / shares * 32);
+#pragma unroll 4
+  for (int i = first * K + threadIdx.x; i < end * K; i += blockDim.x) {
+    const int e = __ldg(idx + i), t = i / K;
+    int row = -1;
+    if (e >= 0 && e < N) {
+      const int at = (t >> 5) * N + e;
+      row = base[e] + wbase[at] + __popc(bits[at] & ((1u << (t & 31)) - 1u));
+      row_token[row] = t0 + t;
+    }
+    slot_pos[(size_t)t0 * K + i] = row;
+  }
+  __syncwarp();
+  cluster_wait();  // the others may still read this CTA's
 }
 
 // A batch of one chunk (T <= 256) together with its copy, in one launch: every
