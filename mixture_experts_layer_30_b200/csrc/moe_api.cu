@@ -480,8 +480,8 @@ moe_status permute_layout(const moe_shape& s, const int32_t* idx, const int32_t*
     if (e != cudaSuccess)
       return fail(MOE_ERR_CUDA, "dispatch layout: %s", cudaGetErrorString(e));
   }
-  // one cluster per 64 of a CTA's tokens, 16 at most: 128 SMs
-  const int shares = std::max(1, std::min(16, per / 64));
+  // one cluster per 64 of a CTA's tokens, 8 at most: 64 SMs
+  const int shares = std::max(1, std::min(8, per / 64));
   const int threads = std::max(256, std::min(1024, per * s.K / 4 / 32 * 32));
   launch_cluster_pdl(moe::perm_cluster_kernel, dim3(moe::kPermCluster * shares), dim3(threads),
                      dim3(moe::kPermCluster), smem, st, idx, s.T, s.K, s.N, s.N + s.Z, per, counts,
