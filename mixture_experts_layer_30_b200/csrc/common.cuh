@@ -71,14 +71,16 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
 }
 
 // --- asynchronous copies to shared memory ------------------------------------
-MOE_DEV void cp_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                   (uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+// Shared-memory addresses as the 32-bit numbers that instructions take.
+MOE_DEV uint32_t smem_at(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+MOE_DEV void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+MOE_DEV void cp_async16(void* dst, const void* src) { cp_async16(smem_at(dst), src); }
 template <int kBytes>  // 4 or 8
-MOE_DEV void cp_async_small(void* dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(
-                   (uint32_t)__cvta_generic_to_shared(dst)), "l"(src), "n"(kBytes) : "memory");
+MOE_DEV void cp_async_small(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes)
+               : "memory");
 }
 MOE_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kPending>  // all but this thread's last kPending groups have landed

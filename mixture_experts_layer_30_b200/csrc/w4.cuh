@@ -16,6 +16,8 @@
 // Scales: [matrix, row block, column block, 16 rows, 128 / G].
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace moe {
@@ -196,7 +198,14 @@ w4_simt_kernel(const T* __restrict__ A, const uint32_t* __restrict__ q0,
 // ---------------------------------------------------------------------------
 constexpr int kW4Warps = 8;
 
-MOE_DEV uint4 w4_lds(const void* p) { return *reinterpret_cast<const uint4*>(p); }
+// (Loads are ordered by the "memory" clobbers of the waits and barriers around a step.)
+template <int kOffset>
+MOE_DEV uint4 w4_lds(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4 + %5];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at), "n"(kOffset));
+  return v;
+}
 
 // The columns (2 i, 2 i + 1) of a code word whose nibbles i and i + 4 lie at bits
 // 4 H .. + 3 of both halves, as a packed bf16 pair of (code - 8) / 64.
@@ -210,16 +219,14 @@ MOE_DEV uint32_t w4_pair(uint32_t w) {
 }
 
 MOE_DEV void w4_mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // the first product of a group: c is only written
 MOE_DEV void w4_mma_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%10, %10, %10, %10};"
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
@@ -229,20 +236,26 @@ MOE_DEV void w4_mma_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, ui
 template <int GPS> struct W4Scale;
 template <> struct W4Scale<1> {
   uint16_t v;
-  MOE_DEV void load(const char* p) { v = *reinterpret_cast<const uint16_t*>(p); }
+  template <int kOffset> MOE_DEV void load(uint32_t at) {
+    asm volatile("ld.shared.u16 %0, [%1 + %2];" : "=h"(v) : "r"(at), "n"(kOffset));
+  }
   MOE_DEV float get(int) const { return __uint_as_float((uint32_t)v << 16); }
 };
 template <> struct W4Scale<2> {
   uint32_t v;
-  MOE_DEV void load(const char* p) { v = *reinterpret_cast<const uint32_t*>(p); }
+  template <int kOffset> MOE_DEV void load(uint32_t at) {
+    asm volatile("ld.shared.u32 %0, [%1 + %2];" : "=r"(v) : "r"(at), "n"(kOffset));
+  }
   MOE_DEV float get(int i) const { return __uint_as_float(i ? v & 0xffff0000u : v << 16); }
 };
 template <> struct W4Scale<4> {
-  uint2 v;
-  MOE_DEV void load(const char* p) { v = *reinterpret_cast<const uint2*>(p); }
+  uint32_t v[2];
+  template <int kOffset> MOE_DEV void load(uint32_t at) {
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2 + %3];"
+                 : "=r"(v[0]), "=r"(v[1]) : "r"(at), "n"(kOffset));
+  }
   MOE_DEV float get(int i) const {
-    const uint32_t w = i < 2 ? v.x : v.y;
-    return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+    return __uint_as_float(i & 1 ? v[i / 2] & 0xffff0000u : v[i / 2] << 16);
   }
 };
 
@@ -351,26 +364,30 @@ MOE_DEV void w4_costs(const W4Problem& p, int* off, int* cost, int* scan_tmp) {
   __syncthreads();
 }
 
-// One step's products of a warp's two row blocks with NT column tiles.
+// One step's products of a warp's two row blocks with NT column tiles.  codes, x: this
+// lane's 16 bytes of the first row half resp. token piece, scales: its row's.
 template <int GPS, int NT>
-MOE_DEV void w4_step(const char* codes, const char* xs, float (&acc)[2][NT][4]) {
-  const int lane = threadIdx.x & 31, g = lane >> 2;
+MOE_DEV void w4_step(uint32_t codes, uint32_t scales, uint32_t xs, float (&acc)[2][NT][4]) {
   constexpr int kPer = 4 / GPS;  // 32-column pieces of one group
+  constexpr int kHalfScales = 8 * GPS * 2;
   uint4 q[2][2];
   W4Scale<GPS> sc[2][2];
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      q[m][h] = w4_lds(codes + m * kW4Block + h * (kW4Block / 2) + lane * 16);
-      sc[m][h].load(codes + 2 * kW4Block + (m * kW4Rows + h * 8 + g) * (GPS * 2));
-    }
+  q[0][0] = w4_lds<0>(codes);
+  q[0][1] = w4_lds<kW4Block / 2>(codes);
+  q[1][0] = w4_lds<kW4Block>(codes);
+  q[1][1] = w4_lds<kW4Block * 3 / 2>(codes);
+  sc[0][0].template load<0>(scales);
+  sc[0][1].template load<kHalfScales>(scales);
+  sc[1][0].template load<2 * kHalfScales>(scales);
+  sc[1][1].template load<3 * kHalfScales>(scales);
   float c[2][NT][4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  auto piece = [&](auto jc) {
+    constexpr int j = decltype(jc)::value;
     uint4 x[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) x[n] = w4_lds(xs + (n * 4 + j) * 512 + lane * 16);
+    x[0] = w4_lds<j * 512>(xs);
+    if constexpr (NT > 1) x[1] = w4_lds<(4 + j) * 512>(xs);
+    if constexpr (NT > 2) x[2] = w4_lds<(8 + j) * 512>(xs);
+    if constexpr (NT > 3) x[3] = w4_lds<(12 + j) * 512>(xs);
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       const uint32_t lo = j == 0 ? q[m][0].x : j == 1 ? q[m][0].y : j == 2 ? q[m][0].z : q[m][0].w;
@@ -380,12 +397,12 @@ MOE_DEV void w4_step(const char* codes, const char* xs, float (&acc)[2][NT][4]) 
       const uint32_t a23[4] = {w4_pair<0>(lo8), w4_pair<0>(hi8), w4_pair<1>(lo8), w4_pair<1>(hi8)};
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        if (j % kPer == 0) w4_mma_first(c[m][n], a01, x[n].x, x[n].y);
+        if constexpr (j % kPer == 0) w4_mma_first(c[m][n], a01, x[n].x, x[n].y);
         else w4_mma(c[m][n], a01, x[n].x, x[n].y);
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n) w4_mma(c[m][n], a23, x[n].z, x[n].w);
-      if (j % kPer == kPer - 1) {
+      if constexpr (j % kPer == kPer - 1) {
         const float s0 = sc[m][0].get(j / kPer), s1 = sc[m][1].get(j / kPer);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -396,7 +413,11 @@ MOE_DEV void w4_step(const char* codes, const char* xs, float (&acc)[2][NT][4]) 
         }
       }
     }
-  }
+  };
+  piece(std::integral_constant<int, 0>{});
+  piece(std::integral_constant<int, 1>{});
+  piece(std::integral_constant<int, 2>{});
+  piece(std::integral_constant<int, 3>{});
 }
 
 // Stores one 16 x 8 piece of the result: output columns c0, c0 + 8 of rows i0, i0 + 1.
@@ -429,19 +450,23 @@ struct W4Kernel {
 
   const W4Problem& p;
   const int *off, *cost;
-  char *codes, *xs;  // this warp's and this slice's ring
   float4* red;       // this pair's
   int rb_n, sp_n, groups, n_steps, ks, wu;
-  // codes: the next step to copy, its addresses
+  // codes: items and steps of the current one that are not copied yet, this lane's next
+  // addresses and where they go (a position of this warp's ring)
   Cursor load;
-  int load_step, load_left, load_slot;
+  int load_left, load_todo;
   const uint8_t *qa, *qb;
   const char* sc;
+  uint32_t ring, ring_end, wr;
+  uint32_t sc_lane;  // from this lane's codes of a stage to its share of the scales
   // token rows: the same, one step ahead of the products
   Cursor xload;
-  int x_step, x_left, x_slot;
+  int x_left, x_todo, x_cols;  // x_cols: columns of k_dim from this lane's on
+  bool x_on;                   // this lane's row exists
   const __nv_bfloat16* xp;
-  int slot, x_read;  // the ring positions of the products
+  uint32_t x_piece;            // where its first piece goes in a buffer
+  uint32_t rd, x_rd, x_both;   // the products' ring position and buffer; both buffers' sum
 
   // A row block past the last repeats it; its results are not stored.
   MOE_DEV int row_block(int group, int m) const {
@@ -459,26 +484,23 @@ struct W4Kernel {
     const int m = lane / kHalf & 1;
     sc = reinterpret_cast<const char*>(m && kGated ? p.s[1] : p.s[0]) +
          (m ? blk[1] : blk[0]) * (kW4Rows * GPS * 2) + (lane % kHalf) * kEach;
+    load_todo = n_steps;
   }
   MOE_DEV void fill_codes() {
     if (load_left > 0) {
-      const int lane = threadIdx.x & 31;
-      char* dst = codes + load_slot * Cfg::kCodeStage;
-      cp_async16(dst + lane * 16, qa);
-      cp_async16(dst + kW4Block / 2 + lane * 16, qa + kW4Block / 2);
-      cp_async16(dst + kW4Block + lane * 16, qb);
-      cp_async16(dst + kW4Block + kW4Block / 2 + lane * 16, qb + kW4Block / 2);
-      if (lane < 2 * kHalf) cp_async_small<kEach>(dst + 2 * kW4Block + lane * kEach, sc);
+      cp_async16(wr, qa);
+      cp_async16(wr + kW4Block / 2, qa + kW4Block / 2);
+      cp_async16(wr + kW4Block, qb);
+      cp_async16(wr + kW4Block * 3 / 2, qb + kW4Block / 2);
+      if (2 * kHalf == 32 || (threadIdx.x & 31) < 2 * kHalf) cp_async_small<kEach>(wr + sc_lane, sc);
       qa += WK * kW4Block;
       qb += WK * kW4Block;
       sc += WK * kW4Rows * GPS * 2;
-      load_slot = load_slot + 1 == D ? 0 : load_slot + 1;
-      if (++load_step == n_steps) {
-        load_step = 0;
-        if (--load_left > 0) {
-          load.next(off, cost, p.N, groups);
-          code_item();
-        }
+      wr += Cfg::kCodeStage;
+      if (wr >= ring_end) wr -= D * Cfg::kCodeStage;
+      if (--load_todo == 0 && --load_left > 0) {
+        load.next(off, cost, p.N, groups);
+        code_item();
       }
     }
     cp_async_commit();
@@ -486,42 +508,47 @@ struct W4Kernel {
 
   // This lane's part of the chunk's token rows: row g of column tile wu / (WR / MaxNT), the
   // pieces from wu % (WR / MaxNT) * kPieces on, eight columns t of each.
-  MOE_DEV void x_item() {
+  MOE_DEV void x_item(bool rows) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int r = wu / (WR / MaxNT) * 8 + g;
-    int row = 0;
-    if (r < xload.rows) {
-      row = xload.r0 + r;
-      if (p.a_rows) {
-        row = p.a_rows[row];
-        if (row < 0 || row >= p.a_src_rows) {
-          set_status(p.status, MOE_DEV_BAD_OFFSETS);
-          row = 0;
+    const int col = ks * kW4Cols + wu % (WR / MaxNT) * kPieces * 32 + 8 * t;
+    if (rows) {
+      const int r = wu / (WR / MaxNT) * 8 + g;
+      int row = 0;
+      x_on = r < xload.rows;
+      if (x_on) {
+        row = xload.r0 + r;
+        if (p.a_rows) {
+          row = p.a_rows[row];
+          if (row < 0 || row >= p.a_src_rows) {
+            set_status(p.status, MOE_DEV_BAD_OFFSETS);
+            row = 0;
+          }
         }
       }
+      xp = p.a + (size_t)row * p.k_dim + col;
+    } else {
+      xp -= n_steps * WK * kW4Cols;
     }
-    xp = p.a + (size_t)row * p.k_dim + ks * kW4Cols + wu % (WR / MaxNT) * kPieces * 32 + 8 * t;
+    x_cols = p.k_dim - col;
+    x_todo = n_steps;
   }
-  MOE_DEV void fill_x() {
+  MOE_DEV void fill_x(uint32_t buffer) {
     if (x_left > 0) {
-      const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-      const int tile = wu / (WR / MaxNT), piece = wu % (WR / MaxNT) * kPieces;
-      if (tile * 8 + g < xload.rows) {
-        char* dst = xs + x_slot * Cfg::kXStage + (tile * 4 + piece) * 512 + lane * 16;
-        const int k = (ks + x_step * WK) * kW4Cols + piece * 32 + 8 * t;
+      if (x_on) {
+        const uint32_t dst = buffer + x_piece;
 #pragma unroll
         for (int j = 0; j < kPieces; ++j) {
-          if (k + 32 * j < p.k_dim) cp_async16(dst + j * 512, xp + x_step * WK * kW4Cols + 32 * j);
-          else *reinterpret_cast<uint4*>(dst + j * 512) = make_uint4(0, 0, 0, 0);
+          if (x_cols > 32 * j) cp_async16(dst + j * 512, xp + 32 * j);
+          else asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst + j * 512), "r"(0)
+                            : "memory");
         }
       }
-      x_slot ^= 1;
-      if (++x_step == n_steps) {
-        x_step = 0;
-        if (--x_left > 0 && xload.next(off, cost, p.N, groups)) {
-          xload.take(off);
-          x_item();
-        }
+      xp += WK * kW4Cols;
+      x_cols -= WK * kW4Cols;
+      if (--x_todo == 0 && --x_left > 0) {
+        const bool rows = xload.next(off, cost, p.N, groups);
+        if (rows) xload.take(off);
+        x_item(rows);
       }
     }
     cp_async_commit();
@@ -542,11 +569,13 @@ struct W4Kernel {
       cp_async_wait<1>();
       // every copy of this step has landed, and the step before is read
       asm volatile("bar.sync %0, %1;" ::"r"(1 + ks), "n"(WR * 32) : "memory");
-      fill_x();
+      const uint32_t other = x_both - x_rd;
+      fill_x(other);
       fill_codes();
-      w4_step<GPS, NT>(codes + slot * Cfg::kCodeStage, xs + x_read * Cfg::kXStage, acc);
-      x_read ^= 1;
-      slot = slot + 1 == D ? 0 : slot + 1;
+      w4_step<GPS, NT>(rd + lane * 16, rd + 2 * kW4Block + (lane >> 2) * (GPS * 2), x_rd, acc);
+      rd += Cfg::kCodeStage;
+      if (rd >= ring_end) rd -= D * Cfg::kCodeStage;
+      x_rd = other;
     }
     auto store = [&](int n, float4 v0, float4 v1) {
       const int u = it.group * WR + wu;
@@ -621,8 +650,8 @@ w4_mma_kernel(const __grid_constant__ W4Problem p) {
   if (left == 0) return;
   cur.take(off);
   const int warp = threadIdx.x >> 5, ks = warp % WK, wu = warp / WK;
-  K k{p, off, cost, w4_smem + warp * Cfg::kDepth * Cfg::kCodeStage,
-      w4_smem + Cfg::kCodes + ks * 2 * Cfg::kXStage,
+  const int lane = threadIdx.x & 31;
+  K k{p, off, cost,
       reinterpret_cast<float4*>(w4_smem + Cfg::kCodes + Cfg::kX + wu * (Cfg::kRed / WR))};
   k.rb_n = rb_n;
   k.sp_n = sp_n;
@@ -630,14 +659,21 @@ w4_mma_kernel(const __grid_constant__ W4Problem p) {
   k.ks = ks;
   k.wu = wu;
   k.n_steps = sp_n > ks ? (sp_n - ks + WK - 1) / WK : 0;
+  k.rd = smem_at(w4_smem) + warp * Cfg::kDepth * Cfg::kCodeStage;
+  k.ring_end = k.rd + Cfg::kDepth * Cfg::kCodeStage;
+  k.wr = k.rd + lane * 16;
+  k.sc_lane = 2 * kW4Block + lane * K::kEach - lane * 16;
+  const uint32_t xbuf = smem_at(w4_smem) + Cfg::kCodes + ks * 2 * Cfg::kXStage + lane * 16;
+  k.x_piece = (wu / (WR / MaxNT) * 4 + wu % (WR / MaxNT) * K::kPieces) * 512;
+  k.x_rd = xbuf;
+  k.x_both = 2 * xbuf + Cfg::kXStage;
   k.load = k.xload = cur;
-  k.load_step = k.load_slot = k.x_step = k.x_slot = k.slot = k.x_read = 0;
   k.load_left = k.x_left = k.n_steps > 0 ? left : 0;
   k.code_item();
 #pragma unroll
   for (int i = 0; i < Cfg::kDepth - 2; ++i) k.fill_codes();
-  k.x_item();
-  k.fill_x();
+  k.x_item(true);
+  k.fill_x(xbuf);
   k.fill_codes();
   for (;;) {
     const int nt = (cur.rows + 7) / 8;
