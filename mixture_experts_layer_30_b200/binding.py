@@ -91,6 +91,7 @@ SIGNATURES = {
 }
 
 _lib = None
+_calls = None
 
 
 class MoEError(RuntimeError):
@@ -112,6 +113,16 @@ def lib():
             fn.restype, fn.argtypes = res, args
         _lib = L
     return _lib
+
+
+def _native():
+    """The module of the short calls (raises if it was not built)."""
+    global _calls
+    if _calls is None:
+        lib()
+        from . import _calls as module
+        _calls = module
+    return _calls
 
 
 def _check(code):
@@ -160,14 +171,10 @@ def _p(t, dtype=None, name="tensor"):
 
 
 def _at(t, dtype, dev, name):
-    """_p of a tensor that has to lie on device `dev`, where the call launches.  (One
-    test of the three properties: the checks of a small call cost more than its kernel.)"""
-    if t is None:
-        return None
-    if t.get_device() == dev and t.dtype is dtype and t.is_contiguous():
-        return t.data_ptr()
+    """_p of a tensor that has to lie on device `dev`, where the call launches."""
     p = _p(t, dtype, name)
-    _here(t)
+    if t is not None and t.get_device() != dev:
+        _here(t)
     return p
 
 
@@ -292,6 +299,10 @@ def forward_mxfp8(buf: "LayerBuffers", fb: Mxfp8Buffers, x, w_router, w1, w3, w2
 def permute_mxfp8_rows(shape, x_q, x_sf, topk_idx, counts, offsets, row_token, slot_pos, x_perm_q,
                        x_perm_sf, ws, stream=None):
     """permute_mxfp8 for tokens held in MXFP8 already (rmsnorm's y_q, y_sf)."""
+    code = _native().permute_mxfp8_rows(shape, x_q, x_sf, topk_idx, counts, offsets, row_token,
+                                        slot_pos, x_perm_q, x_perm_sf, ws, stream)
+    if code >= 0:
+        return _check(code)
     dev = torch.cuda.current_device()
     u8, i32 = torch.uint8, torch.int32
     _check(lib().moe_permute_mxfp8_rows(ctypes.byref(shape), _at(x_q, u8, dev, "x_q"),
@@ -343,6 +354,9 @@ def _w4(pair, n, rows, cols, group, name, dev=None):
 def expert_gate_up_w4(shape, group, x, row_token, w1, w3, offsets, h, ws, stream=None):
     """w1, w3: (codes, scales) pairs from quantize_weights_w4; row_token None: x is
     x_perm."""
+    code = _native().expert_gate_up_w4(shape, group, x, row_token, w1, w3, offsets, h, ws, stream)
+    if code >= 0:
+        return _check(code)
     dt, dev = torch_dtype(shape), torch.cuda.current_device()
     N, I, d = shape.N, shape.I, shape.d
     q1, s1 = _w4(w1, N, I, d, group, "w1", dev)
@@ -355,6 +369,9 @@ def expert_gate_up_w4(shape, group, x, row_token, w1, w3, offsets, h, ws, stream
 
 
 def expert_down_w4(shape, group, h, w2, offsets, y_perm, ws, stream=None):
+    code = _native().expert_down_w4(shape, group, h, w2, offsets, y_perm, ws, stream)
+    if code >= 0:
+        return _check(code)
     dt, dev = torch_dtype(shape), torch.cuda.current_device()
     q2, s2 = _w4(w2, shape.N, shape.d, shape.I, group, "w2", dev)
     _check(lib().moe_expert_down_w4(ctypes.byref(shape), group, _at(h, dt, dev, "h"), q2, s2,
@@ -389,6 +406,10 @@ def rmsnorm(x, weight, eps, y, residual=None, sum_out=None, inv_rms=None, y_q=No
     """y = RMS norm of x (+ residual) times weight; sum_out receives x + residual,
     inv_rms the row factors, y_q and y_sf the rounded y in MXFP8.  y may be None
     when y_q is given."""
+    code = _native().rmsnorm(x, weight, eps, y, residual, sum_out, inv_rms, y_q, y_sf,
+                             stream)
+    if code >= 0:
+        return _check(code)
     T, d, code = _rows(x)
     dt, dev, f32, u8 = x.dtype, torch.cuda.current_device(), torch.float32, torch.uint8
     _same(x, (("residual", residual), ("sum_out", sum_out), ("y", y)))
@@ -413,6 +434,9 @@ def new_rmsnorm_workspace(T: int, d: int, device="cuda") -> torch.Tensor:
 def rmsnorm_backward(s, weight, inv_rms, dy, dx, dweight, ws, dsum=None, stream=None):
     """Gradients of rmsnorm: s is its sum_out (x without a residual), dsum the
     gradient along the residual stream; dx is the gradient of x and of residual."""
+    code = _native().rmsnorm_backward(s, weight, inv_rms, dy, dx, dweight, ws, dsum, stream)
+    if code >= 0:
+        return _check(code)
     T, d, code = _rows(s)
     dt, dev = s.dtype, torch.cuda.current_device()
     _same(s, (("dy", dy), ("dx", dx), ("dsum", dsum)))
@@ -532,18 +556,26 @@ def _norm_args(grads, norm):
 
 def gradient_norm(grads: GradientList, norm, stream=None):
     """norm[0] = the 2-norm of all gradients together (fp32, on the device)."""
-    n, table, np, ws = _norm_args(grads, norm)
-    _check(lib().moe_grad_norm(n, table, np, ws, grads.ws.numel(), _stream(stream)))
+    code = _native().clip_gradients(len(grads.tensors), grads.table, None, norm, grads.ws, stream)
+    if code < 0:
+        n, table, np, ws = _norm_args(grads, norm)
+        code = lib().moe_grad_norm(n, table, np, ws, grads.ws.numel(), _stream(stream))
+    _check(code)
     return norm
 
 
 def clip_gradients(grads: GradientList, max_norm, norm, stream=None):
     """Scales the gradients by min(1, max_norm / (norm + 1e-6)) into grads.out, with
     their global norm, which is left in norm[0]."""
-    n, table, np, ws = _norm_args(grads, norm)
-    st, L = _stream(stream), lib()
-    _check(L.moe_grad_norm(n, table, np, ws, grads.ws.numel(), st))
-    _check(L.moe_grad_clip(n, table, float(max_norm), np, st))
+    max_norm = float(max_norm)
+    code = _native().clip_gradients(len(grads.tensors), grads.table, max_norm, norm, grads.ws,
+                                    stream)
+    if code < 0:
+        n, table, np, ws = _norm_args(grads, norm)
+        st, L = _stream(stream), lib()
+        _check(L.moe_grad_norm(n, table, np, ws, grads.ws.numel(), st))
+        code = L.moe_grad_clip(n, table, max_norm, np, st)
+    _check(code)
     return norm
 
 

@@ -1,4 +1,4 @@
-"""Builds libmoe_b200.so (sm_100a) in-tree with nvcc.
+"""Builds libmoe_b200.so (sm_100a) and the binding's native module _calls.so in-tree.
 
     python -m mixture_experts_layer_30_b200.build
 
@@ -9,12 +9,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_b200.so")
+CALLS = os.path.join(PKG, "_calls.so")
+CALLS_SRC = os.path.join(CSRC, "calls.cpp")
 SOURCES = [os.path.join(CSRC, "moe_api.cu"), os.path.join(CSRC, "block_api.cu")]
 
 
@@ -48,8 +51,31 @@ def _stale(obj: str) -> bool:
                for n in names + [os.path.abspath(__file__)])
 
 
+def _calls_commands():
+    """Compile and link commands of _calls.so: a CPython module on torch's tensors that
+    calls libmoe_b200.so beside it."""
+    import torch
+    home = os.path.dirname(torch.__file__)
+    obj = _object_of(CALLS_SRC)
+    compile_cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-DNDEBUG",
+                   f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                   "-I", os.path.join(ROOT, "include"),
+                   "-isystem", sysconfig.get_paths()["include"],
+                   "-isystem", os.path.join(home, "include"),
+                   "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+                   "-isystem", os.path.join(os.path.dirname(os.path.dirname(nvcc_path())),
+                                            "include"),
+                   "-MD", "-MF", obj + ".d", "-c", CALLS_SRC, "-o", obj + ".tmp"]
+    link_cmd = [compile_cmd[0], "-shared", "-o", CALLS + ".tmp", obj, LIB,
+                "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda",
+                "-lc10", "-Wl,-rpath,$ORIGIN"]
+    return obj, compile_cmd, link_cmd
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _newest_input_mtime():
+    newest = _newest_input_mtime()
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= newest
+                         for f in (LIB, CALLS)):
         return LIB
     os.makedirs(OBJ, exist_ok=True)
     base = [nvcc_path(), "-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo",
@@ -64,6 +90,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
             cmd = base + ["-MD", "-MF", obj + ".d", "-c", src, "-o", obj + ".tmp"]
             runs.append((obj, subprocess.Popen(cmd, stdout=subprocess.PIPE,
                                                stderr=subprocess.STDOUT, text=True)))
+    calls_obj, calls_compile, calls_link = _calls_commands()
+    if force or _stale(calls_obj):
+        runs.append((calls_obj, subprocess.Popen(calls_compile, stdout=subprocess.PIPE,
+                                                 stderr=subprocess.STDOUT, text=True)))
     failed = ""
     for obj, proc in runs:
         out, _ = proc.communicate()
@@ -74,13 +104,14 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         else:
             os.replace(obj + ".tmp", obj)
     if failed:
-        raise RuntimeError("nvcc failed:\n" + failed)
-    tmp = LIB + ".tmp"
-    res = subprocess.run(base + ["-shared", "-o", tmp] + [_object_of(s) for s in SOURCES],
-                         capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError("link failed:\n" + (res.stdout + res.stderr)[-4000:])
-    os.replace(tmp, LIB)
+        raise RuntimeError("compilation failed:\n" + failed)
+    soname = ["-Xlinker", "-soname=" + os.path.basename(LIB)]
+    for out, cmd in ((LIB, base + ["-shared", "-o", LIB + ".tmp"] + soname
+                      + [_object_of(s) for s in SOURCES]), (CALLS, calls_link)):
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError("link failed:\n" + (res.stdout + res.stderr)[-4000:])
+        os.replace(out + ".tmp", out)
     return LIB
 
 
