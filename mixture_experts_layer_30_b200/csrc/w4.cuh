@@ -285,7 +285,7 @@ struct W4Cfg {
   static constexpr int kBytes = kCodes + kX + kRed;  // and two tables of N + 1 and 33 ints
   // Cost of a chunk of nt column tiles: decoding the codes against their products, as the
   // times of one to four tiles stand to one another.
-  static MOE_DEV int weight(int rows) { return 5 + 2 * ((rows + 7) / 8); }
+  static MOE_DEV int weight(int rows) { return NT == 1 ? 1 : 5 + 2 * ((rows + 7) / 8); }
 };
 
 // An item: WR pairs of row blocks (group) for one chunk of an expert's rows.
@@ -304,15 +304,19 @@ struct W4Cursor {
     do ++e;
     while (e < N && cost[e + 1] == cost[e]);
   }
-  // The first item that starts at or behind `at` in the order of all costs.
-  MOE_DEV void seek(const int* off, const int* cost, int N, int groups, long long at) {
+  // The first item that starts at or behind part / parts of all costs (U holds their product
+  // with parts: 32 bits where they do, for the divisions' latency).
+  template <typename U>
+  MOE_DEV void seek(const int* off, const int* cost, int N, int groups, int part, int parts) {
+    const U at = (U)cost[N] * groups * part / parts;
     c = group = 0;
     e = N;
-    if (at >= (long long)cost[N] * groups) return;
+    if (part == parts || at >= (U)cost[N] * groups) return;
     e = find_expert(cost, N, (int)(at / groups));
-    long long rem = at - (long long)cost[e] * groups;
-    const long long full = (long long)Cfg::weight(Cfg::kRows) * groups;
-    c = (int)min(rem / full, (long long)((off[e + 1] - off[e] - 1) / Cfg::kRows));
+    U rem = at - (U)cost[e] * groups;
+    const U full = (U)Cfg::weight(Cfg::kRows) * groups;
+    const int last = (off[e + 1] - off[e] - 1) / Cfg::kRows;
+    if (last > 0) c = (int)min(rem / full, (U)last);
     rem -= c * full;
     take(off);
     const int w = Cfg::weight(rows);
@@ -355,7 +359,7 @@ MOE_DEV void w4_costs(const W4Problem& p, int* off, int* cost, int* scan_tmp) {
   int run = block_exclusive_scan(local, scan_tmp, &scan_tmp[32]);
   for (int e = lo; e < hi; ++e) {
     cost[e] = run;
-    run += weigh(e, false);
+    if (per > 1) run += weigh(e, false);
   }
   if (threadIdx.x == 0) {
     cost[p.N] = scan_tmp[32];
@@ -641,10 +645,20 @@ w4_mma_kernel(const __grid_constant__ W4Problem p) {
   const int rb_n = w4_row_blocks(p.n_out), sp_n = w4_col_blocks(p.k_dim);
   const int units = kGated ? rb_n : (rb_n + 1) / 2;
   const int groups = (units + WR - 1) / WR;
-  const long long total = (long long)cost[p.N] * groups;
+  // even lanes look for the start of this CTA's run, odd ones for its end
   typename K::Cursor cur, end;
-  cur.seek(off, cost, p.N, groups, total * blockIdx.x / gridDim.x);
-  end.seek(off, cost, p.N, groups, total * (blockIdx.x + 1) / gridDim.x);
+  const int part = blockIdx.x + (threadIdx.x & 1);
+  if ((long long)cost[p.N] * groups * gridDim.x < (1LL << 32))
+    end.template seek<uint32_t>(off, cost, p.N, groups, part, gridDim.x);
+  else
+    end.template seek<unsigned long long>(off, cost, p.N, groups, part, gridDim.x);
+  auto from = [](int v, int lane) { return __shfl_sync(0xffffffffu, v, lane); };
+  cur.e = from(end.e, 0);
+  cur.c = from(end.c, 0);
+  cur.group = from(end.group, 0);
+  end.e = from(end.e, 1);
+  end.c = from(end.c, 1);
+  end.group = from(end.group, 1);
   int left = 0;
   for (typename K::Cursor c = cur; !c.same(end); ++left) c.next(off, cost, p.N, groups);
   if (left == 0) return;
