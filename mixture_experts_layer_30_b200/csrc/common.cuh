@@ -77,6 +77,11 @@ MOE_DEV void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 MOE_DEV void cp_async16(void* dst, const void* src) { cp_async16(smem_at(dst), src); }
+// Zeros, without reading src, where `read` is false.
+MOE_DEV void cp_async16_or_zero(uint32_t dst, const void* src, bool read) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(read ? 16 : 0) : "memory");
+}
 template <int kBytes>  // 4 or 8
 MOE_DEV void cp_async_small(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes)

@@ -207,6 +207,18 @@ MOE_DEV uint4 w4_lds(uint32_t at) {
   return v;
 }
 
+// (a, b) += s * (x, y) in one instruction, each rounded as fmaf does.
+MOE_DEV uint64_t w4_two(float a, float b) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  return v;
+}
+MOE_DEV void w4_fma2(float& a, float& b, uint64_t s, float x, float y) {
+  uint64_t v = w4_two(a, b);
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(v) : "l"(s), "l"(w4_two(x, y)));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+
 // The columns (2 i, 2 i + 1) of a code word whose nibbles i and i + 4 lie at bits
 // 4 H .. + 3 of both halves, as a packed bf16 pair of (code - 8) / 64.
 template <int H>
@@ -285,7 +297,7 @@ struct W4Cfg {
   static constexpr int kBytes = kCodes + kX + kRed;  // and two tables of N + 1 and 33 ints
   // Cost of a chunk of nt column tiles: decoding the codes against their products, as the
   // times of one to four tiles stand to one another.
-  static MOE_DEV int weight(int rows) { return NT == 1 ? 1 : 5 + 2 * ((rows + 7) / 8); }
+  static MOE_DEV int weight(int rows) { return NT == 1 ? 1 : rows <= 8 ? 5 : rows <= 16 ? 6 : rows <= 24 ? 8 : 10; }
 };
 
 // An item: WR pairs of row blocks (group) for one chunk of an expert's rows.
@@ -369,8 +381,9 @@ MOE_DEV void w4_costs(const W4Problem& p, int* off, int* cost, int* scan_tmp) {
 }
 
 // One step's products of a warp's two row blocks with NT column tiles.  codes, x: this
-// lane's 16 bytes of the first row half resp. token piece, scales: its row's.
-template <int GPS, int NT>
+// lane's 16 bytes of the first row half resp. token piece, scales: its row's.  kPairs: the
+// scaled sums two at a time (with several column tiles the pairs' registers cost more).
+template <int GPS, int NT, bool kPairs>
 MOE_DEV void w4_step(uint32_t codes, uint32_t scales, uint32_t xs, float (&acc)[2][NT][4]) {
   constexpr int kPer = 4 / GPS;  // 32-column pieces of one group
   constexpr int kHalfScales = 8 * GPS * 2;
@@ -407,13 +420,22 @@ MOE_DEV void w4_step(uint32_t codes, uint32_t scales, uint32_t xs, float (&acc)[
 #pragma unroll
       for (int n = 0; n < NT; ++n) w4_mma(c[m][n], a23, x[n].z, x[n].w);
       if constexpr (j % kPer == kPer - 1) {
-        const float s0 = sc[m][0].get(j / kPer), s1 = sc[m][1].get(j / kPer);
+        const float f0 = sc[m][0].get(j / kPer), f1 = sc[m][1].get(j / kPer);
+        if constexpr (kPairs) {
+          const uint64_t s0 = w4_two(f0, f0), s1 = w4_two(f1, f1);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          acc[m][n][0] = fmaf(s0, c[m][n][0], acc[m][n][0]);
-          acc[m][n][1] = fmaf(s0, c[m][n][1], acc[m][n][1]);
-          acc[m][n][2] = fmaf(s1, c[m][n][2], acc[m][n][2]);
-          acc[m][n][3] = fmaf(s1, c[m][n][3], acc[m][n][3]);
+          for (int n = 0; n < NT; ++n) {
+            w4_fma2(acc[m][n][0], acc[m][n][1], s0, c[m][n][0], c[m][n][1]);
+            w4_fma2(acc[m][n][2], acc[m][n][3], s1, c[m][n][2], c[m][n][3]);
+          }
+        } else {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            acc[m][n][0] = fmaf(f0, c[m][n][0], acc[m][n][0]);
+            acc[m][n][1] = fmaf(f0, c[m][n][1], acc[m][n][1]);
+            acc[m][n][2] = fmaf(f1, c[m][n][2], acc[m][n][2]);
+            acc[m][n][3] = fmaf(f1, c[m][n][3], acc[m][n][3]);
+          }
         }
       }
     }
@@ -542,9 +564,7 @@ struct W4Kernel {
         const uint32_t dst = buffer + x_piece;
 #pragma unroll
         for (int j = 0; j < kPieces; ++j) {
-          if (x_cols > 32 * j) cp_async16(dst + j * 512, xp + 32 * j);
-          else asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst + j * 512), "r"(0)
-                            : "memory");
+          cp_async16_or_zero(dst + j * 512, xp + 32 * j, x_cols > 32 * j);
         }
       }
       xp += WK * kW4Cols;
@@ -576,7 +596,7 @@ struct W4Kernel {
       const uint32_t other = x_both - x_rd;
       fill_x(other);
       fill_codes();
-      w4_step<GPS, NT>(rd + lane * 16, rd + 2 * kW4Block + (lane >> 2) * (GPS * 2), x_rd, acc);
+      w4_step<GPS, NT, MaxNT == 1>(rd + lane * 16, rd + 2 * kW4Block + (lane >> 2) * (GPS * 2), x_rd, acc);
       rd += Cfg::kCodeStage;
       if (rd >= ring_end) rd -= D * Cfg::kCodeStage;
       x_rd = other;
