@@ -138,6 +138,45 @@ MOE_DEV uint4 pack16(const float* f, __nv_bfloat16) {
                     pack_bf16x2(f[6], f[7]));
 }
 
+// --- pairs of fp32 --------------------------------------------------------------
+// Two fp32 values in one 64-bit register; an operation on both is one instruction and
+// rounds each as the scalar operation does.
+MOE_DEV uint64_t f2_pack(float a, float b) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  return v;
+}
+MOE_DEV void f2_unpack(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+MOE_DEV uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t v;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
+}
+MOE_DEV uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t v;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+  return v;
+}
+// A 16-byte vector as pairs.
+MOE_DEV void unpack16_f2(const uint4& v, uint64_t* f, float) {
+  f[0] = f2_pack(__uint_as_float(v.x), __uint_as_float(v.y));
+  f[1] = f2_pack(__uint_as_float(v.z), __uint_as_float(v.w));
+}
+MOE_DEV void unpack16_f2(const uint4& v, uint64_t* f, __nv_bfloat16) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    f[i] = f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+template <typename T> MOE_DEV uint4 pack16_f2(const uint64_t* f) {
+  float o[16 / sizeof(T)];
+#pragma unroll
+  for (int i = 0; i < (int)(8 / sizeof(T)); ++i) f2_unpack(f[i], o[2 * i], o[2 * i + 1]);
+  return pack16(o, T());
+}
+
 // SiLU(a) = a * sigmoid(a) = a / (1 + e^-a); for a -> -inf, e^-a = inf gives -0.
 MOE_DEV float silu(float a) { return a / (1.0f + expf(-a)); }
 

@@ -174,8 +174,11 @@ rmsnorm_kernel(const T* x, const T* res, const T* __restrict__ w, float eps, int
 // row is kept in global memory (each thread adds to its own columns).
 constexpr int kBwdDepth = 3;
 
+// Threads of a CTA at most: up to two vectors a thread, two CTAs of an SM share its registers.
+constexpr int bwd_threads(int vpt) { return vpt == 1 || vpt == 2 ? 384 : 512; }
+
 template <typename T, int VPT, bool kSum>
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__(bwd_threads(VPT), VPT == 1 || VPT == 2 ? 2 : 1)
 rmsnorm_bwd_kernel(const T* s, const T* __restrict__ w, const float* __restrict__ inv_rms,
                    const T* dy, const T* dsum, int rows, int d, T* dx, float* __restrict__ part) {
   pdl_trigger();
@@ -211,8 +214,9 @@ rmsnorm_bwd_kernel(const T* s, const T* __restrict__ w, const float* __restrict_
       }
       cp_async_commit();
     };
+    constexpr int VP = VN / 2;  // pairs of a vector
     uint4 wr[VPT];
-    float dw[VPT][VN];
+    uint64_t dw[VPT][VP];
 #pragma unroll
     for (int k = 0; k < kBwdDepth - 1; ++k) fetch(first + k * stride, k);
 #pragma unroll
@@ -220,7 +224,7 @@ rmsnorm_bwd_kernel(const T* s, const T* __restrict__ w, const float* __restrict_
       const int v = tid + i * step;
       wr[i] = v < nvec ? __ldg(wv + v) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int k = 0; k < VN; ++k) dw[i][k] = 0.f;
+      for (int k = 0; k < VP; ++k) dw[i][k] = 0;
     }
     int stage = 0;
     // the loop runs by the CTA's first row: its groups keep step with one another
@@ -231,43 +235,42 @@ rmsnorm_bwd_kernel(const T* s, const T* __restrict__ w, const float* __restrict_
       const bool live = r < n_rows;
       const float inv = live ? inv_rms[r] : 0.f;
       cp_async_wait<kBwdDepth - 1>();
-      uint4 cs[VPT], cy[VPT];
-      float c = 0.f;
+      const uint64_t inv2 = f2_pack(inv, inv);
+      uint64_t xh[VPT][VP], wg[VPT][VP], c2 = 0;  // xhat and w dy, kept over the reduction
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int v = tid + i * step;
         if (live && v < nvec) {
-          cs[i] = *slot(stage, 0, i);
-          cy[i] = *slot(stage, 1, i);
-          float f[VN], g[VN], ww[VN];
-          unpack16(cs[i], f, T());
-          unpack16(cy[i], g, T());
-          unpack16(wr[i], ww, T());
+          uint64_t g[VP];
+          unpack16_f2(*slot(stage, 0, i), xh[i], T());
+          unpack16_f2(*slot(stage, 1, i), g, T());
+          unpack16_f2(wr[i], wg[i], T());
 #pragma unroll
-          for (int k = 0; k < VN; ++k) {
-            const float p = g[k] * (f[k] * inv);
-            c = fmaf(ww[k], p, c);
-            dw[i][k] += p;
+          for (int k = 0; k < VP; ++k) {
+            xh[i][k] = f2_mul(xh[i][k], inv2);
+            wg[i][k] = f2_mul(wg[i][k], g[k]);
+            c2 = f2_fma(wg[i][k], xh[i][k], c2);
+            dw[i][k] = f2_fma(g[k], xh[i][k], dw[i][k]);
           }
         }
       }
-      c = row_sum(c, red[flip] + 32 * threadIdx.y) / (float)d;
+      float c, c_odd;
+      f2_unpack(c2, c, c_odd);
+      c = row_sum(c + c_odd, red[flip] + 32 * threadIdx.y) / (float)d;
       flip ^= 1;
+      const uint64_t minus_c = f2_pack(-c, -c);
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int v = tid + i * step;
         if (!live || v >= nvec) continue;
-        float f[VN], g[VN], ww[VN], o[VN];
-        unpack16(cs[i], f, T());
-        unpack16(cy[i], g, T());
-        unpack16(wr[i], ww, T());
-        if constexpr (kSum) unpack16(*slot(stage, 2, i), o, T());
+        uint64_t o[VP];
+        if constexpr (kSum) unpack16_f2(*slot(stage, 2, i), o, T());
 #pragma unroll
-        for (int k = 0; k < VN; ++k) {
-          const float t = inv * (ww[k] * g[k] - f[k] * inv * c);
-          o[k] = kSum ? o[k] + t : t;
+        for (int k = 0; k < VP; ++k) {
+          const uint64_t t = f2_fma(xh[i][k], minus_c, wg[i][k]);
+          o[k] = kSum ? f2_fma(t, inv2, o[k]) : f2_mul(t, inv2);
         }
-        reinterpret_cast<uint4*>(dx + (size_t)r * d)[v] = pack16(o, T());
+        reinterpret_cast<uint4*>(dx + (size_t)r * d)[v] = pack16_f2<T>(o);
       }
       stage = stage + 1 == kBwdDepth ? 0 : stage + 1;
     }
@@ -275,36 +278,30 @@ rmsnorm_bwd_kernel(const T* s, const T* __restrict__ w, const float* __restrict_
     if (blockDim.y > 1) {
       cp_async_wait<0>();
       __syncthreads();
-      float4* all = reinterpret_cast<float4*>(ring);  // [group][VPT][VN / 4][blockDim.x]
-      constexpr int kQ = VN / 4;
+      uint64_t* all = reinterpret_cast<uint64_t*>(ring);  // [group][VPT][VP][blockDim.x]
 #pragma unroll
       for (int i = 0; i < VPT; ++i)
 #pragma unroll
-        for (int k = 0; k < kQ; ++k)
-          all[((threadIdx.y * VPT + i) * kQ + k) * step + tid] = make_float4(
-              dw[i][4 * k], dw[i][4 * k + 1], dw[i][4 * k + 2], dw[i][4 * k + 3]);
+        for (int k = 0; k < VP; ++k)
+          all[((threadIdx.y * VPT + i) * VP + k) * step + tid] = dw[i][k];
       __syncthreads();
       if (threadIdx.y > 0) return;
+      const uint64_t one = f2_pack(1.f, 1.f);
       for (int y = 1; y < (int)blockDim.y; ++y)
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
 #pragma unroll
-          for (int k = 0; k < kQ; ++k) {
-            const float4 o = all[((y * VPT + i) * kQ + k) * step + tid];
-            dw[i][4 * k] += o.x;
-            dw[i][4 * k + 1] += o.y;
-            dw[i][4 * k + 2] += o.z;
-            dw[i][4 * k + 3] += o.w;
-          }
+          for (int k = 0; k < VP; ++k)
+            dw[i][k] = f2_fma(all[((y * VPT + i) * VP + k) * step + tid], one, dw[i][k]);
     }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = tid + i * step;
       if (v >= nvec) continue;
 #pragma unroll
-      for (int k = 0; k < VN; k += 4)
-        reinterpret_cast<float4*>(mine)[(v * VN + k) / 4] =
-            make_float4(dw[i][k], dw[i][k + 1], dw[i][k + 2], dw[i][k + 3]);
+      for (int k = 0; k < VP; k += 2)
+        reinterpret_cast<ulonglong2*>(mine)[(v * VN) / 4 + k / 2] =
+            make_ulonglong2(dw[i][k], dw[i][k + 1]);
     }
   } else {
     for (int j = tid; j < nvec; j += step)

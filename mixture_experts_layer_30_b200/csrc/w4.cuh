@@ -207,16 +207,9 @@ MOE_DEV uint4 w4_lds(uint32_t at) {
   return v;
 }
 
-// (a, b) += s * (x, y) in one instruction, each rounded as fmaf does.
-MOE_DEV uint64_t w4_two(float a, float b) {
-  uint64_t v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
-  return v;
-}
+// (a, b) += s * (x, y) as one instruction on pairs.
 MOE_DEV void w4_fma2(float& a, float& b, uint64_t s, float x, float y) {
-  uint64_t v = w4_two(a, b);
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(v) : "l"(s), "l"(w4_two(x, y)));
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+  f2_unpack(f2_fma(s, f2_pack(x, y), f2_pack(a, b)), a, b);
 }
 
 // The columns (2 i, 2 i + 1) of a code word whose nibbles i and i + 4 lie at bits
@@ -422,7 +415,7 @@ MOE_DEV void w4_step(uint32_t codes, uint32_t scales, uint32_t xs, float (&acc)[
       if constexpr (j % kPer == kPer - 1) {
         const float f0 = sc[m][0].get(j / kPer), f1 = sc[m][1].get(j / kPer);
         if constexpr (kPairs) {
-          const uint64_t s0 = w4_two(f0, f0), s1 = w4_two(f1, f1);
+          const uint64_t s0 = f2_pack(f0, f0), s1 = f2_pack(f1, f1);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             w4_fma2(acc[m][n][0], acc[m][n][1], s0, c[m][n][0], c[m][n][1]);
