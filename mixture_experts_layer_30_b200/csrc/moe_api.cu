@@ -446,8 +446,9 @@ moe_status permute_impl(const moe_shape& s, const void* x, const int32_t* idx,
     int dev = 0;
     cudaGetDevice(&dev);
     if (smem > 48 * 1024 && dev < 64 && !g_rank_attr_set[dev]) {
+      // for the most experts: set once, it has to serve every later shape
       cudaFuncSetAttribute(moe::perm_rank_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)smem);
+                           16 * moe::kMaxExperts * (int)sizeof(uint32_t));
       g_rank_attr_set[dev] = true;
     }
     moe::launch_pdl(moe::perm_rank_kernel, dim3(nch), dim3(256), smem, st, idx, s.T, s.K, s.N, E, cbase, row_token,

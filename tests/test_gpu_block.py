@@ -183,3 +183,14 @@ def test_training_step():
     for a, b in zip(before, grads):
         np.testing.assert_allclose(b.double().cpu().numpy(), a.double().cpu().numpy() * coef,
                                    rtol=2.0 ** -21, atol=1e-38)
+
+
+def test_dispatch_of_more_experts_than_the_call_before():
+    """Large shared tables: a call with more experts follows one with fewer."""
+    for N in (900, 1000, 1024):
+        shape, x, idx, counts = routed(600, 256, N, 0, 2, N)
+        ws = B.new_workspace(shape)
+        want = dispatch(shape, lambda *o: B.permute_mxfp8(shape, x, idx, counts, *o, ws))
+        off = torch.zeros(N + 1, dtype=torch.int32, device="cuda")
+        off[1:] = counts[:N].cumsum(0)
+        assert torch.equal(want[0], off) and B.device_status(ws) == 0
