@@ -173,7 +173,7 @@ struct NormBwdArgs {
 template <typename T, int VPT, bool kSum>
 cudaError_t norm_bwd_launch(const NormBwdArgs& a, int threads, int groups, int* ctas) {
   auto* kernel = moe::rmsnorm_bwd_kernel<T, VPT, kSum>;
-  const int smem = moe::kBwdDepth * (kSum ? 3 : 2) * VPT * threads * groups * 16;
+  const int smem = moe::bwd_depth(VPT) * (kSum ? 3 : 2) * VPT * threads * groups * 16;
   // CTAs that an SM holds: by the ring, and by the 512 threads x 128 registers that the
   // kernel may take
   const int fit = smem ? (224 * 1024) / (smem + 2048) : 4;

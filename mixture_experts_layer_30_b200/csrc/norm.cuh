@@ -167,12 +167,13 @@ rmsnorm_kernel(const T* x, const T* res, const T* __restrict__ w, float eps, int
 // Backward: the CTA's blockDim.y row groups take rows base + group, base advancing
 // by the grid; a thread owns the same columns in every row, so dw accumulates in
 // registers and a CTA writes one fp32 partial row.  A thread copies its own
-// vectors of s, dy and dsum into its own slots of a shared-memory ring kBwdDepth - 1
+// vectors of s, dy and dsum into its own slots of a shared-memory ring kDepth - 1
 // rows ahead (cp.async, no barrier: nobody else reads them), so the copies of the
 // next rows run under this row's reduction, which is the only block-wide wait.
 // VPT = 0: rows longer than the ring holds; they are read twice and the partial
 // row is kept in global memory (each thread adds to its own columns).
-constexpr int kBwdDepth = 3;
+// Rows in the ring: four vectors a thread (wide rows) leave room for two.
+__host__ __device__ constexpr int bwd_depth(int vpt) { return vpt == 4 ? 2 : 3; }
 
 // Threads of a CTA at most: up to two vectors a thread, two CTAs of an SM share its registers.
 constexpr int bwd_threads(int vpt) { return vpt == 1 || vpt == 2 ? 384 : 512; }
@@ -190,8 +191,8 @@ rmsnorm_bwd_kernel(const T* s, const T* __restrict__ w, const float* __restrict_
   float* mine = part + (size_t)blockIdx.x * d;
   int flip = 0;
   if constexpr (VPT > 0) {
-    constexpr int kIn = kSum ? 3 : 2;
-    extern __shared__ uint4 ring[];  // [kBwdDepth][kIn][VPT][threads]
+    constexpr int kIn = kSum ? 3 : 2, kDepth = bwd_depth(VPT);
+    extern __shared__ uint4 ring[];  // [kDepth][kIn][VPT][threads]
     const int threads = blockDim.x * blockDim.y, me = threadIdx.y * blockDim.x + tid;
     // unsigned: the fetch runs past a row count next to 2^31
     const unsigned n_rows = rows, stride = gridDim.x * blockDim.y;
@@ -218,7 +219,7 @@ rmsnorm_bwd_kernel(const T* s, const T* __restrict__ w, const float* __restrict_
     uint4 wr[VPT];
     uint64_t dw[VPT][VP];
 #pragma unroll
-    for (int k = 0; k < kBwdDepth - 1; ++k) fetch(first + k * stride, k);
+    for (int k = 0; k < kDepth - 1; ++k) fetch(first + k * stride, k);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = tid + i * step;
@@ -230,11 +231,11 @@ rmsnorm_bwd_kernel(const T* s, const T* __restrict__ w, const float* __restrict_
     // the loop runs by the CTA's first row: its groups keep step with one another
     for (unsigned base = blockIdx.x * blockDim.y, r = first; base < n_rows;
          base += stride, r += stride) {
-      const int ahead = stage ? stage - 1 : kBwdDepth - 1;  // the slots of the row before
-      fetch(r + (kBwdDepth - 1) * stride, ahead);
+      const int ahead = stage ? stage - 1 : kDepth - 1;  // the slots of the row before
+      fetch(r + (kDepth - 1) * stride, ahead);
       const bool live = r < n_rows;
       const float inv = live ? inv_rms[r] : 0.f;
-      cp_async_wait<kBwdDepth - 1>();
+      cp_async_wait<kDepth - 1>();
       const uint64_t inv2 = f2_pack(inv, inv);
       uint64_t xh[VPT][VP], wg[VPT][VP], c2 = 0;  // xhat and w dy, kept over the reduction
 #pragma unroll
@@ -272,7 +273,7 @@ rmsnorm_bwd_kernel(const T* s, const T* __restrict__ w, const float* __restrict_
         }
         reinterpret_cast<uint4*>(dx + (size_t)r * d)[v] = pack16_f2<T>(o);
       }
-      stage = stage + 1 == kBwdDepth ? 0 : stage + 1;
+      stage = stage + 1 == kDepth ? 0 : stage + 1;
     }
     // one partial row a CTA: the groups' sums joined in group order
     if (blockDim.y > 1) {
