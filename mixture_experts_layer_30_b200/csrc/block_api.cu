@@ -277,8 +277,11 @@ moe_status w4_mma(const moe_shape& s, const W4Args& a) {
   auto items = [&](int rows, int wr) {
     return (std::min<long long>(s.N, max_rows) + max_rows / rows) * ((units + wr - 1) / wr);
   };
-  // Mean rows of an expert at most 4: one column tile holds nearly every expert's.
-  if (max_rows <= 4LL * (s.N + s.Z)) {
+  // Chunks of 8 rows (one column tile) or of 16, by the mean rows of an expert, for gate/up:
+  // 3.25 of them (13 tokens at d = 6144, I = 2048, N = 32) 89 against 98 us, 4 (64 tokens of
+  // the mid layer) 37 against 31.  Chunks of 32 spread skewed loads worse: 63 against 57 us at
+  // 256 tokens of the mid layer.
+  if (2 * max_rows <= 7LL * (s.N + s.Z)) {
     // Four pairs in two slices join half as often as two pairs in four, but cut the work in
     // pieces of twice the size: with four pieces and more a CTA (of the experts that K of E
     // choices a token are expected to touch) 46 -> 44 us for the down product of 13 tokens at
@@ -288,7 +291,7 @@ moe_status w4_mma(const moe_shape& s, const W4Args& a) {
       return w4_launch<GPS, kGated, 4, 1>(p, items(8, 4), a.st);
     return w4_launch<GPS, kGated, 2, 1>(p, items(8, 2), a.st);
   }
-  return w4_launch<GPS, kGated, 4, 4>(p, items(32, 4), a.st);
+  return w4_launch<GPS, kGated, 4, 2>(p, items(16, 4), a.st);
 }
 
 template <bool kGated>

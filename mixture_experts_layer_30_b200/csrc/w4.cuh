@@ -175,8 +175,15 @@ w4_simt_kernel(const T* __restrict__ A, const uint32_t* __restrict__ q0,
 // A decode batch gives an expert a few rows, so the weights are the traffic: an
 // expert's codes are streamed once and every other cost has to stay below that
 // stream.  The weights are the 16-row operand of mma.m16n8k16 (M = output rows),
-// the tokens its 8 columns; up to 4 column tiles (32 rows of an expert) share one
-// pass over the codes.
+// the tokens its 8 columns; up to 2 column tiles (16 rows of an expert) share one
+// pass over the codes.  Bound by instruction issue: a step below takes 280 to 340
+// instructions a warp, 144 of them to decode, and four warps a scheduler reach 0.6 of
+// the issue rate.  Down product at d = 6144, I = 2048, N = 32, 13 tokens, groups of 32:
+// 44 us, 5.1 TB/s; gate/up of the mid layer (64 x 2048 x 1024) at 256 tokens, groups of
+// 64: 58 us, 2.5 TB/s.  The same products on tcgen05 (codes decoded into tensor memory,
+// the groups' sums read back for their scales) took longer up to 24 rows an expert: 60
+// against 48 us at 16 rows; a half step's chain of store, barrier, products and sums is
+// longer than its decoding.
 //   * A warp's step is two row blocks x 128 columns (2 KiB of codes).  A lane holds
 //     16 bytes of a row: columns 32 j + 8 t .. + 7 for j = 0..3.  The order of a
 //     contraction is free, so the instruction's k slots are given the columns as
@@ -193,8 +200,9 @@ w4_simt_kernel(const T* __restrict__ A, const uint32_t* __restrict__ q0,
 //   * Items (row chunk of an expert, WR pairs of row blocks) are cut into contiguous
 //     runs of equal cost, one per CTA.  Codes and scales come through a ring of
 //     shared-memory stages (cp.async) filled two steps ahead across items, token rows
-//     (from L2) one step ahead; a warp's codes are its own, a token tile
-//     is shared by the WR warps of a slice.
+//     (from L2) one step ahead; a warp's codes are its own, a token tile is shared by
+//     the WR warps of a slice.  A third resident CTA with shorter rings was slower (77
+//     against 57 us at 256 tokens of the mid layer), a deeper ring not faster.
 // ---------------------------------------------------------------------------
 constexpr int kW4Warps = 8;
 
@@ -288,9 +296,9 @@ struct W4Cfg {
   static constexpr int kX = kWk * 2 * kXStage;
   static constexpr int kRed = (kWk - 1) * WR * 2 * NT * 512;
   static constexpr int kBytes = kCodes + kX + kRed;  // and two tables of N + 1 and 33 ints
-  // Cost of a chunk of nt column tiles: decoding the codes against their products, as the
-  // times of one to four tiles stand to one another.
-  static MOE_DEV int weight(int rows) { return NT == 1 ? 1 : rows <= 8 ? 5 : rows <= 16 ? 6 : rows <= 24 ? 8 : 10; }
+  // Cost of a chunk: 8 rows against 16 an expert take 35 and 44 us for the mid layer's
+  // gate/up (64 experts, 2048 x 1024, groups of 128), of which about 5 are the call's.
+  static MOE_DEV int weight(int rows) { return NT == 1 ? 1 : rows <= 8 ? 5 : 6; }
 };
 
 // An item: WR pairs of row blocks (group) for one chunk of an expert's rows.
@@ -396,8 +404,6 @@ MOE_DEV void w4_step(uint32_t codes, uint32_t scales, uint32_t xs, float (&acc)[
     uint4 x[NT];
     x[0] = w4_lds<j * 512>(xs);
     if constexpr (NT > 1) x[1] = w4_lds<(4 + j) * 512>(xs);
-    if constexpr (NT > 2) x[2] = w4_lds<(8 + j) * 512>(xs);
-    if constexpr (NT > 3) x[3] = w4_lds<(12 + j) * 512>(xs);
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       const uint32_t lo = j == 0 ? q[m][0].x : j == 1 ? q[m][0].y : j == 2 ? q[m][0].z : q[m][0].w;
@@ -589,7 +595,7 @@ struct W4Kernel {
       const uint32_t other = x_both - x_rd;
       fill_x(other);
       fill_codes();
-      w4_step<GPS, NT, MaxNT == 1>(rd + lane * 16, rd + 2 * kW4Block + (lane >> 2) * (GPS * 2), x_rd, acc);
+      w4_step<GPS, NT, MaxNT == 1 || GPS != 1>(rd + lane * 16, rd + 2 * kW4Block + (lane >> 2) * (GPS * 2), x_rd, acc);
       rd += Cfg::kCodeStage;
       if (rd >= ring_end) rd -= D * Cfg::kCodeStage;
       x_rd = other;
@@ -704,10 +710,8 @@ w4_mma_kernel(const __grid_constant__ W4Problem p) {
   k.fill_codes();
   for (;;) {
     const int nt = (cur.rows + 7) / 8;
-    if (MaxNT == 1 || nt <= 1) k.template item<1>(cur);
-    else if (MaxNT >= 2 && nt == 2) k.template item<MaxNT >= 2 ? 2 : 1>(cur);
-    else if (MaxNT >= 3 && nt == 3) k.template item<MaxNT >= 3 ? 3 : 1>(cur);
-    else if (MaxNT >= 4) k.template item<MaxNT >= 4 ? 4 : 1>(cur);
+    if (nt <= 1) k.template item<1>(cur);
+    else k.template item<MaxNT>(cur);
     if (--left == 0) break;
     if (cur.next(off, cost, p.N, groups)) cur.take(off);
   }
