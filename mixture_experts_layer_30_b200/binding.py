@@ -194,6 +194,8 @@ def _rows(x):
     if x.dim() != 2 or x.dtype not in _DTYPE_CODES:
         raise ValueError(f"rows must be a 2-d float32 or bfloat16 tensor, not {x.dtype} "
                          f"{tuple(x.shape)}")
+    if max(x.shape) > 0x7fffffff:  # ctypes would cut it to 32 bits
+        raise ValueError(f"rows {tuple(x.shape)}: more than 2^31 - 1 rows or columns")
     return x.shape[0], x.shape[1], _DTYPE_CODES[x.dtype]
 
 

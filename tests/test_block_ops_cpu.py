@@ -235,3 +235,10 @@ def test_binding_checks_sizes_before_the_call():
     with pytest.raises(ValueError, match="do not hold"):
         B._w4((torch.zeros(1024, dtype=torch.uint8), torch.zeros(16, dtype=torch.bfloat16)), 1, 17,
               128, 128, "w1")
+
+
+@pytest.mark.parametrize("shape", [(2 ** 31, 8), (2 ** 32 + 5, 8), (1, 2 ** 32 + 8)])
+def test_rows_past_32_bits_are_refused(shape):
+    """As 32-bit numbers these would be negative or another, small size."""
+    with pytest.raises(ValueError, match="more than"):
+        B._rows(torch.empty(shape, dtype=torch.bfloat16, device="meta"))
