@@ -472,9 +472,9 @@ size_t moe_rmsnorm_workspace_bytes(int32_t T, int32_t d);
  *   dx = inv_rms * (weight * dy - xhat * mean_j(weight * dy * xhat)) + dsum
  *   dweight[j] = sum_t dy[t, j] * xhat[t, j]
  * dx is the gradient of x and of residual.  s is sum_out of the forward call (x
- * without a residual), inv_rms its output.  Sums are fp32 in a fixed order; dx
- * [T, d] and dweight [d] have the dtype and are rounded once.  dx may be dy or
- * dsum.  With T == 0 dweight is set to zero. */
+ * without a residual), inv_rms its output.  Sums are fp32 in a fixed order (the
+ * last of an fp32 dweight fp64); dx [T, d] and dweight [d] have the dtype and are
+ * rounded once.  dx may be dy or dsum.  With T == 0 dweight is set to zero. */
 moe_status moe_rmsnorm_backward(int32_t T, int32_t d, int32_t dtype, const void* s,
                                 const void* weight, const float* inv_rms, const void* dy,
                                 const void* dsum, void* dx, void* dweight, void* ws,
@@ -505,8 +505,9 @@ moe_status moe_grad_norm(int32_t n_tensors, const moe_grad* list, float* norm, v
 
 /* out = grad * min(1, max_norm / (*norm + 1e-6)), rounded once; norm is a device
  * pointer (of moe_grad_norm, or a norm joined over ranks).  A NaN norm makes every
- * element NaN; an infinite one makes finite elements 0.  When the factor is 1 and
- * every tensor is clipped in place, nothing is written. */
+ * element NaN; an infinite one makes finite elements 0 (NaN where max_norm is
+ * infinite too).  When the factor is 1 and every tensor is clipped in place, nothing
+ * is written. */
 moe_status moe_grad_clip(int32_t n_tensors, const moe_grad* list, float max_norm,
                          const float* norm, void* stream);
 

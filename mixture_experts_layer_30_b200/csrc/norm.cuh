@@ -19,6 +19,8 @@
 // loads: 641 us).
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "quant.cuh"
 
@@ -350,15 +352,17 @@ rmsnorm_bwd_kernel(const T* s, const T* __restrict__ w, const float* __restrict_
 }
 
 // dw[j] = sum over the n partial rows in a fixed order: 32 columns a CTA, 32
-// warps that each sum every 32nd row, joined in warp order.  n = 0 gives 0.
+// warps that each sum every 32nd row, joined by one warp a column: in fp64 for an fp32
+// dw (333 x 1000: error against 64 bits 7.5e-8 of the norm, 1.3e-7 with a join in fp32).
+// n = 0 gives 0.
 template <typename T>
 __global__ void __launch_bounds__(1024)
 rmsnorm_dw_kernel(const float* __restrict__ part, int n, int d, T* __restrict__ dw) {
   pdl_trigger();
   pdl_wait();
-  __shared__ float acc[32][32];
+  __shared__ float acc[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int j = blockIdx.x * 32 + lane;
+  const int j = blockIdx.x * 32 + lane, mine = blockIdx.x * 32 + warp;
   float v = 0.f;
   if (j < d) {
 #pragma unroll 8
@@ -366,12 +370,10 @@ rmsnorm_dw_kernel(const float* __restrict__ part, int n, int d, T* __restrict__ 
   }
   acc[warp][lane] = v;
   __syncthreads();
-  if (warp == 0 && j < d) {
-    float t = acc[0][lane];
+  std::conditional_t<sizeof(T) == 4, double, float> t = acc[lane][warp];
 #pragma unroll
-    for (int k = 1; k < 32; ++k) t += acc[k][lane];
-    dw[j] = Cvt<T>::from_f(t);
-  }
+  for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  if (lane == 0 && mine < d) dw[mine] = Cvt<T>::from_f((float)t);
 }
 
 }  // namespace moe

@@ -225,3 +225,14 @@ def test_norm_backward_widths(d, dtype):
         each = dy.double() * xhat
         tol = (each.sum(0).abs() * half + each.abs().sum(0) * (T + 24) * u32) * (1 + 2.0 ** -7)
         assert ((dw.double() - each.sum(0)).abs() <= tol).all()
+
+
+def test_infinite_max_norm_leaves_the_gradients():
+    """The factor is 1 then, and inf / inf = NaN for an infinite norm."""
+    g = torch.linspace(-3, 3, 1001, device="cuda")
+    out, norm = torch.empty_like(g), torch.empty(1, device="cuda")
+    B.clip_gradients(B.GradientList([g], out=[out]), float("inf"), norm)
+    assert torch.equal(out, g) and torch.isfinite(norm).all()
+    g[500] = float("inf")
+    B.clip_gradients(B.GradientList([g], out=[out]), float("inf"), norm)
+    assert torch.isinf(norm).all() and torch.isnan(out).all()
