@@ -211,6 +211,11 @@ def _size(t, n, name):
         raise ValueError(f"{name} has {t.numel()} elements, expected {n}")
 
 
+def _holds(t, n, name):
+    if t is not None and t.numel() < n:
+        raise ValueError(f"{name} has {t.numel()} elements, expected at least {n}")
+
+
 def _stream(stream=None):
     """Handle of `stream` or of torch's current stream (read directly: building a
     torch.cuda.Stream for it takes longer than a launch)."""
@@ -305,6 +310,8 @@ def permute_mxfp8_rows(shape, x_q, x_sf, topk_idx, counts, offsets, row_token, s
                                         slot_pos, x_perm_q, x_perm_sf, ws, stream)
     if code >= 0:
         return _check(code)
+    _holds(x_q, shape.T * shape.d, "x_q")
+    _holds(x_sf, shape.T * shape.d // 32, "x_sf")
     dev = torch.cuda.current_device()
     u8, i32 = torch.uint8, torch.int32
     _check(lib().moe_permute_mxfp8_rows(ctypes.byref(shape), _at(x_q, u8, dev, "x_q"),

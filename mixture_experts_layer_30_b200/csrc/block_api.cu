@@ -304,11 +304,15 @@ moe_status w4_product(const moe_shape& s, const W4Args& a) {
   }
 }
 
-// I is the contraction of the second half: its rows are read 16 bytes at a time.
+// I is the contraction of the second half: its rows are read 16 bytes at a time.  A chunk's
+// end is a 32-bit row number, up to kW4Tile behind the last row.
 moe_status check_w4_shape(const moe_shape& s) {
   const int vec = s.dtype == MOE_BF16 ? 8 : 4;
   if (s.I % vec)
     return fail(MOE_ERR_UNSUPPORTED, "I=%d must be a multiple of %d for 16-byte rows", s.I, vec);
+  if ((long long)s.T * s.K > 0x7fffffffLL - moe::kW4Tile)
+    return fail(MOE_ERR_UNSUPPORTED, "T*K=%lld routed rows leave a chunk's end past int32",
+                (long long)s.T * s.K);
   return MOE_OK;
 }
 

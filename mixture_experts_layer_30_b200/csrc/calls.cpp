@@ -193,6 +193,9 @@ PyObject* permute_mxfp8_rows(PyObject*, PyObject* const* v, Py_ssize_t n) {
     Args a(v, n, 12);
     size_t bytes;
     const moe_shape s = a.shape();
+    const int64_t codes = (int64_t)s.T * s.d;
+    if (THPVariable_Check(v[1]) && THPVariable_Unpack(v[1]).numel() < codes) throw Refused();
+    if (THPVariable_Check(v[2]) && THPVariable_Unpack(v[2]).numel() < codes / 32) throw Refused();
     void* q = a.ptr(at::kByte);
     void* sf = a.ptr(at::kByte);
     auto idx = (const int32_t*)a.ptr(at::kInt);

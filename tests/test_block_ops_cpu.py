@@ -242,3 +242,24 @@ def test_rows_past_32_bits_are_refused(shape):
     """As 32-bit numbers these would be negative or another, small size."""
     with pytest.raises(ValueError, match="more than"):
         B._rows(torch.empty(shape, dtype=torch.bfloat16, device="meta"))
+
+
+@pytest.mark.parametrize("T,K", [(2 ** 31 - 1, 1), (2 ** 30 - 32, 2)])
+def test_w4_rows_next_to_32_bits_are_refused(lib, T, K):
+    """The end of the last chunk would not be a 32-bit number."""
+    s = B.make_shape(T, 8, 2, 0, K, 8, "bf16")
+    for code in (lib.moe_expert_gate_up_w4(ctypes.byref(s), 32, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE,
+                                           FAKE, FAKE, FAKE, BIG, None),
+                 lib.moe_expert_down_w4(ctypes.byref(s), 32, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE,
+                                        BIG, None)):
+        assert code == UNSUPPORTED and b"past int32" in lib.moe_last_error()
+
+
+@pytest.mark.parametrize("rows,blocks,name", [(15, 16 * 8, "x_q"), (16, 16 * 8 - 1, "x_sf")])
+def test_dispatch_of_short_8bit_rows_is_refused(lib, rows, blocks, name):
+    """Codes or scales of fewer tokens than the shape has would be read past their end."""
+    s = B.make_shape(16, 256, 4, 2, 2, 128, "bf16")
+    q, sf = torch.zeros((rows, 256), dtype=torch.uint8), torch.zeros(blocks, dtype=torch.uint8)
+    ints, out = torch.zeros(64, dtype=torch.int32), torch.zeros(64, dtype=torch.uint8)
+    with pytest.raises(ValueError, match=f"{name} has"):
+        B.permute_mxfp8_rows(s, q, sf, ints, ints, ints, ints, ints, out, out, out)
