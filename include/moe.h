@@ -310,6 +310,15 @@ moe_status moe_expert_gate_up_w4(const moe_shape* shape, int32_t group, const vo
                                  const void* w3_q, const void* w3_s, const int32_t* offsets,
                                  void* h, void* ws, size_t ws_bytes, void* stream);
 
+/* moe_expert_gate_up_w4 on n_rows <= T * K routed rows, the number that row_token
+ * (or x_perm) and h hold: an expert whose rows end behind them counts as empty and
+ * sets MOE_DEV_BAD_OFFSETS. */
+moe_status moe_expert_gate_up_w4_rows(const moe_shape* shape, int32_t group, int32_t n_rows,
+                                      const void* x, const int32_t* row_token, const void* w1_q,
+                                      const void* w1_s, const void* w3_q, const void* w3_s,
+                                      const int32_t* offsets, void* h, void* ws, size_t ws_bytes,
+                                      void* stream);
+
 /* y_perm[r, :] = h[r, :] W2_e^T on 4-bit weights.  Rows >= offsets[N] are not
  * written. */
 moe_status moe_expert_down_w4(const moe_shape* shape, int32_t group, const void* h,

@@ -49,6 +49,8 @@ SIGNATURES = {
                                                _vp]),
     "moe_expert_gate_up_w4": (ctypes.c_int, [_SP, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                              _vp, _sz, _vp]),
+    "moe_expert_gate_up_w4_rows": (ctypes.c_int, [_SP, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
+                                                  _vp, _vp, _vp, _sz, _vp]),
     "moe_expert_down_w4": (ctypes.c_int, [_SP, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "moe_rmsnorm": (ctypes.c_int, [_i32, _i32, _i32, _vp, _vp, _vp, _f32, _vp, _vp, _vp, _vp,
                                    _vp, _vp]),
@@ -310,8 +312,13 @@ def permute_mxfp8_rows(shape, x_q, x_sf, topk_idx, counts, offsets, row_token, s
                                         slot_pos, x_perm_q, x_perm_sf, ws, stream)
     if code >= 0:
         return _check(code)
-    _holds(x_q, shape.T * shape.d, "x_q")
-    _holds(x_sf, shape.T * shape.d // 32, "x_sf")
+    rows = shape.T * shape.K
+    for t, n, name in ((x_q, shape.T * shape.d, "x_q"), (x_sf, shape.T * shape.d // 32, "x_sf"),
+                       (topk_idx, rows, "topk_idx"), (counts, shape.N + shape.Z, "counts"),
+                       (offsets, shape.N + 1, "offsets"), (row_token, rows, "row_token"),
+                       (slot_pos, rows, "slot_pos"), (x_perm_q, rows * shape.d, "x_perm_q"),
+                       (x_perm_sf, rows * shape.d // 32, "x_perm_sf")):
+        _holds(t, n, name)
     dev = torch.cuda.current_device()
     u8, i32 = torch.uint8, torch.int32
     _check(lib().moe_permute_mxfp8_rows(ctypes.byref(shape), _at(x_q, u8, dev, "x_q"),
@@ -362,25 +369,35 @@ def _w4(pair, n, rows, cols, group, name, dev=None):
 
 def expert_gate_up_w4(shape, group, x, row_token, w1, w3, offsets, h, ws, stream=None):
     """w1, w3: (codes, scales) pairs from quantize_weights_w4; row_token None: x is
-    x_perm."""
+    x_perm.  row_token may hold fewer entries than T * K: an expert whose rows end
+    behind them counts as empty and is reported (DEV_BAD_OFFSETS)."""
     code = _native().expert_gate_up_w4(shape, group, x, row_token, w1, w3, offsets, h, ws, stream)
     if code >= 0:
         return _check(code)
+    N, I, d, rows = shape.N, shape.I, shape.d, shape.T * shape.K
+    _holds(x, (rows if row_token is None else shape.T) * d, "x")
+    _holds(offsets, N + 1, "offsets")
+    _holds(h, rows * I, "h")
+    n_rows = min(rows if row_token is None else min(rows, row_token.numel()), 0x7fffffff)
     dt, dev = torch_dtype(shape), torch.cuda.current_device()
-    N, I, d = shape.N, shape.I, shape.d
     q1, s1 = _w4(w1, N, I, d, group, "w1", dev)
     q3, s3 = _w4(w3, N, I, d, group, "w3", dev)
-    _check(lib().moe_expert_gate_up_w4(ctypes.byref(shape), group, _at(x, dt, dev, "x"),
-                                       _at(row_token, torch.int32, dev, "row_token"), q1, s1, q3,
-                                       s3, _at(offsets, torch.int32, dev, "offsets"),
-                                       _at(h, dt, dev, "h"), _at(ws, torch.uint8, dev, "ws"),
-                                       ws.numel(), _stream(stream)))
+    _check(lib().moe_expert_gate_up_w4_rows(ctypes.byref(shape), group, n_rows,
+                                            _at(x, dt, dev, "x"),
+                                            _at(row_token, torch.int32, dev, "row_token"), q1, s1,
+                                            q3, s3, _at(offsets, torch.int32, dev, "offsets"),
+                                            _at(h, dt, dev, "h"), _at(ws, torch.uint8, dev, "ws"),
+                                            ws.numel(), _stream(stream)))
 
 
 def expert_down_w4(shape, group, h, w2, offsets, y_perm, ws, stream=None):
     code = _native().expert_down_w4(shape, group, h, w2, offsets, y_perm, ws, stream)
     if code >= 0:
         return _check(code)
+    rows = shape.T * shape.K
+    _holds(h, rows * shape.I, "h")
+    _holds(offsets, shape.N + 1, "offsets")
+    _holds(y_perm, rows * shape.d, "y_perm")
     dt, dev = torch_dtype(shape), torch.cuda.current_device()
     q2, s2 = _w4(w2, shape.N, shape.d, shape.I, group, "w2", dev)
     _check(lib().moe_expert_down_w4(ctypes.byref(shape), group, _at(h, dt, dev, "h"), q2, s2,

@@ -228,6 +228,7 @@ struct W4Args {
   const int32_t* a_rows;
   const void *q0, *s0, *q1, *s1;
   const int32_t* offsets;
+  int rows;  // routed rows that the buffers hold
   int n_out, k_dim, gps;
   void* c;
   uint32_t* status;
@@ -244,7 +245,7 @@ moe_status w4_simt(const moe_shape& s, const W4Args& a) {
       moe::launch_pdl(moe::w4_simt_kernel<T, kGated>, dim3((unsigned)grid), dim3(256), 0, a.st,
                       static_cast<const T*>(a.a), static_cast<const uint32_t*>(a.q0),
                       static_cast<const __nv_bfloat16*>(a.s0), static_cast<const uint32_t*>(a.q1),
-                      static_cast<const __nv_bfloat16*>(a.s1), a.offsets, s.N, (int)max_rows,
+                      static_cast<const __nv_bfloat16*>(a.s1), a.offsets, s.N, a.rows,
                       a.n_out, a.k_dim, a.gps, static_cast<T*>(a.c), a.status, a.a_rows, s.T),
       kGated ? "4-bit gate/up" : "4-bit down");
 }
@@ -269,7 +270,7 @@ moe_status w4_mma(const moe_shape& s, const W4Args& a) {
                          {static_cast<const __nv_bfloat16*>(a.s0),
                           static_cast<const __nv_bfloat16*>(a.s1)},
                          static_cast<const __nv_bfloat16*>(a.a), a.a_rows, a.offsets, s.N,
-                         s.T * s.K, s.T, a.n_out, a.k_dim, static_cast<__nv_bfloat16*>(a.c),
+                         a.rows, s.T, a.n_out, a.k_dim, static_cast<__nv_bfloat16*>(a.c),
                          a.status};
   const long long rb = moe::w4_row_blocks(a.n_out), units = kGated ? rb : (rb + 1) / 2;
   const long long max_rows = (long long)s.T * s.K;
@@ -476,12 +477,27 @@ moe_status moe_expert_gate_up_w4(const moe_shape* shape, int32_t group, const vo
                                  const int32_t* row_token, const void* w1_q, const void* w1_s,
                                  const void* w3_q, const void* w3_s, const int32_t* offsets,
                                  void* h, void* ws, size_t ws_bytes, void* stream) {
+  const int64_t rows = shape ? (int64_t)shape->T * shape->K : 0;
+  // more rows than 32 bits hold: the shape is refused, whatever the count
+  return moe_expert_gate_up_w4_rows(shape, group, (int32_t)std::min<int64_t>(rows, INT32_MAX), x,
+                                    row_token, w1_q, w1_s, w3_q, w3_s, offsets, h, ws, ws_bytes,
+                                    stream);
+}
+
+moe_status moe_expert_gate_up_w4_rows(const moe_shape* shape, int32_t group, int32_t n_rows,
+                                      const void* x, const int32_t* row_token, const void* w1_q,
+                                      const void* w1_s, const void* w3_q, const void* w3_s,
+                                      const int32_t* offsets, void* h, void* ws, size_t ws_bytes,
+                                      void* stream) {
   MOE_ENTRY("moe_expert_gate_up_w4");
   uint32_t* status = nullptr;
   MOE_TRY(moe::api::layer_status(shape, ws, ws_bytes, &status));
   const moe_shape& s = *shape;
   MOE_TRY(check_group(group));
   MOE_TRY(check_w4_shape(s));
+  if (n_rows < 0 || n_rows > (long long)s.T * s.K)
+    return fail(MOE_ERR_INVALID_ARG, "n_rows=%d outside [0, T*K=%lld]", n_rows,
+                (long long)s.T * s.K);
   MOE_TRY(need(w1_q, "w1_q", 16));
   MOE_TRY(need(w1_s, "w1_s", 16));
   MOE_TRY(need(w3_q, "w3_q", 16));
@@ -491,8 +507,8 @@ moe_status moe_expert_gate_up_w4(const moe_shape* shape, int32_t group, const vo
   MOE_TRY(need(x, "x", 16));
   MOE_TRY(optional(row_token, "row_token", 4));
   MOE_TRY(need(h, "h", 16));
-  return w4_product<true>(s, W4Args{x, row_token, w1_q, w1_s, w3_q, w3_s, offsets, s.I, s.d,
-                                    moe::kW4Cols / group, h, status,
+  return w4_product<true>(s, W4Args{x, row_token, w1_q, w1_s, w3_q, w3_s, offsets, n_rows, s.I,
+                                    s.d, moe::kW4Cols / group, h, status,
                                     static_cast<cudaStream_t>(stream)});
 }
 
@@ -511,8 +527,8 @@ moe_status moe_expert_down_w4(const moe_shape* shape, int32_t group, const void*
   if (s.T == 0) return MOE_OK;
   MOE_TRY(need(h, "h", 16));
   MOE_TRY(need(y_perm, "y_perm", 16));
-  return w4_product<false>(s, W4Args{h, nullptr, w2_q, w2_s, nullptr, nullptr, offsets, s.d, s.I,
-                                     moe::kW4Cols / group, y_perm, status,
+  return w4_product<false>(s, W4Args{h, nullptr, w2_q, w2_s, nullptr, nullptr, offsets, s.T * s.K,
+                                     s.d, s.I, moe::kW4Cols / group, y_perm, status,
                                      static_cast<cudaStream_t>(stream)});
 }
 

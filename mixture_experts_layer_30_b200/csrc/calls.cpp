@@ -10,6 +10,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cstring>
 
 #include "moe.h"
@@ -38,18 +39,24 @@ struct Args {
       throw Refused();
     return t;
   }
-  // Device pointer of the next argument; numel -1: of any size.
-  void* ptr(at::ScalarType type, int64_t numel = -1) {
+  // Device pointer of the next argument, a tensor of numel elements.
+  void* ptr(at::ScalarType type, int64_t numel) {
     const at::Tensor& t = tensor(next(), type);
-    if (numel >= 0 && t.numel() != numel) throw Refused();
+    if (t.numel() != numel) throw Refused();
     return t.data_ptr();
   }
-  void* opt(at::ScalarType type, int64_t numel = -1) {
-    if (v[at] == Py_None) {
-      ++at;
-      return nullptr;
-    }
-    return ptr(type, numel);
+  // Whether the next argument is None, which is passed over then.
+  bool none() {
+    if (v[at] != Py_None) return false;
+    ++at;
+    return true;
+  }
+  void* opt(at::ScalarType type, int64_t numel) { return none() ? nullptr : ptr(type, numel); }
+  // Of a tensor of at least `least` elements.
+  void* holding(at::ScalarType type, int64_t least) {
+    const at::Tensor& t = tensor(next(), type);
+    if (t.numel() < least) throw Refused();
+    return t.data_ptr();
   }
   // Of a tensor with the shape of x.
   void* like(const at::Tensor& x, bool none_ok) {
@@ -125,6 +132,14 @@ W4 w4(Args& a, int64_t n, int64_t rows, int64_t cols, int32_t group) {
   return {q.data_ptr(), s.data_ptr()};
 }
 
+// Routed rows T * K of a shape whose sizes fit 64 bits when multiplied by a row's length.
+int64_t routed_rows(const moe_shape& s) {
+  if (s.T < 0 || s.K < 0 || s.N < 0 || s.Z < 0 || s.d < 0 || s.I < 0) throw Refused();
+  const int64_t rows = (int64_t)s.T * s.K;
+  if (rows > INT32_MAX) throw Refused();
+  return rows;
+}
+
 at::ScalarType layer_type(const moe_shape& s) {
   return s.dtype == MOE_BF16 ? at::kBFloat16 : at::kFloat;
 }
@@ -193,18 +208,16 @@ PyObject* permute_mxfp8_rows(PyObject*, PyObject* const* v, Py_ssize_t n) {
     Args a(v, n, 12);
     size_t bytes;
     const moe_shape s = a.shape();
-    const int64_t codes = (int64_t)s.T * s.d;
-    if (THPVariable_Check(v[1]) && THPVariable_Unpack(v[1]).numel() < codes) throw Refused();
-    if (THPVariable_Check(v[2]) && THPVariable_Unpack(v[2]).numel() < codes / 32) throw Refused();
-    void* q = a.ptr(at::kByte);
-    void* sf = a.ptr(at::kByte);
-    auto idx = (const int32_t*)a.ptr(at::kInt);
-    auto counts = (const int32_t*)a.opt(at::kInt);
-    auto offsets = (int32_t*)a.ptr(at::kInt);
-    auto row_token = (int32_t*)a.ptr(at::kInt);
-    auto slot_pos = (int32_t*)a.ptr(at::kInt);
-    void* oq = a.ptr(at::kByte);
-    void* osf = a.ptr(at::kByte);
+    const int64_t rows = routed_rows(s), codes = (int64_t)s.T * s.d;
+    void* q = a.holding(at::kByte, codes);
+    void* sf = a.holding(at::kByte, codes / 32);
+    auto idx = (const int32_t*)a.holding(at::kInt, rows);
+    auto counts = (const int32_t*)(a.none() ? nullptr : a.holding(at::kInt, (int64_t)s.N + s.Z));
+    auto offsets = (int32_t*)a.holding(at::kInt, (int64_t)s.N + 1);
+    auto row_token = (int32_t*)a.holding(at::kInt, rows);
+    auto slot_pos = (int32_t*)a.holding(at::kInt, rows);
+    void* oq = a.holding(at::kByte, rows * s.d);
+    void* osf = a.holding(at::kByte, rows * s.d / 32);
     void* ws = a.workspace(&bytes);
     void* st = a.stream();
     return [=] {
@@ -220,16 +233,24 @@ PyObject* expert_gate_up_w4(PyObject*, PyObject* const* v, Py_ssize_t n) {
     size_t bytes;
     const moe_shape s = a.shape();
     const int32_t group = a.integer();
-    void* x = a.ptr(layer_type(s));
-    auto row_token = (const int32_t*)a.opt(at::kInt);
+    const int64_t rows = routed_rows(s);
+    const bool in_place = v[3] == Py_None;  // x is x_perm
+    void* x = a.holding(layer_type(s), (in_place ? rows : s.T) * s.d);
+    const int32_t* row_token = nullptr;
+    int32_t n_rows = (int32_t)rows;
+    if (!a.none()) {
+      const at::Tensor& t = a.tensor(a.next(), at::kInt);
+      row_token = (const int32_t*)t.data_ptr();
+      n_rows = (int32_t)std::min(rows, t.numel());
+    }
     const W4 w1 = w4(a, s.N, s.I, s.d, group), w3 = w4(a, s.N, s.I, s.d, group);
-    auto offsets = (const int32_t*)a.ptr(at::kInt);
-    void* h = a.ptr(layer_type(s));
+    auto offsets = (const int32_t*)a.holding(at::kInt, (int64_t)s.N + 1);
+    void* h = a.holding(layer_type(s), rows * s.I);
     void* ws = a.workspace(&bytes);
     void* st = a.stream();
     return [=] {
-      return moe_expert_gate_up_w4(&s, group, x, row_token, w1.q, w1.s, w3.q, w3.s, offsets, h, ws,
-                                   bytes, st);
+      return moe_expert_gate_up_w4_rows(&s, group, n_rows, x, row_token, w1.q, w1.s, w3.q, w3.s,
+                                        offsets, h, ws, bytes, st);
     };
   });
 }
@@ -240,10 +261,11 @@ PyObject* expert_down_w4(PyObject*, PyObject* const* v, Py_ssize_t n) {
     size_t bytes;
     const moe_shape s = a.shape();
     const int32_t group = a.integer();
-    void* h = a.ptr(layer_type(s));
+    const int64_t rows = routed_rows(s);
+    void* h = a.holding(layer_type(s), rows * s.I);
     const W4 w2 = w4(a, s.N, s.d, s.I, group);
-    auto offsets = (const int32_t*)a.ptr(at::kInt);
-    void* y = a.ptr(layer_type(s));
+    auto offsets = (const int32_t*)a.holding(at::kInt, (int64_t)s.N + 1);
+    void* y = a.holding(layer_type(s), rows * s.d);
     void* ws = a.workspace(&bytes);
     void* st = a.stream();
     return [=] { return moe_expert_down_w4(&s, group, h, w2.q, w2.s, offsets, y, ws, bytes, st); };

@@ -1,0 +1,74 @@
+"""Host-side checks of the operators around the layer at their edges: every tensor that is
+too short for its shape is refused before anything is launched (no GPU needed)."""
+import ctypes
+
+import pytest
+import torch
+
+from mixture_experts_layer_30_b200 import binding as B
+from mixture_experts_layer_30_b200 import build as BUILD
+
+FAKE = ctypes.c_void_p(0x10000)
+U8, I32, BF16 = torch.uint8, torch.int32, torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def lib():
+    BUILD.build()
+    return B.lib()
+
+
+def flat(n, dtype):
+    return torch.zeros(n, dtype=dtype)
+
+
+T, D, N, Z, K, I = 16, 256, 4, 2, 2, 128
+R = T * K
+DISPATCH = {"x_q": (T * D, U8), "x_sf": (T * D // 32, U8), "topk_idx": (R, I32),
+            "counts": (N + Z, I32), "offsets": (N + 1, I32), "row_token": (R, I32),
+            "slot_pos": (R, I32), "x_perm_q": (R * D, U8), "x_perm_sf": (R * D // 32, U8)}
+
+
+@pytest.mark.parametrize("name", sorted(DISPATCH))
+def test_short_tensors_of_the_8bit_dispatch_are_refused(lib, name):
+    """The kernels' extents come from the shape alone: one element less would be read or
+    written past its end."""
+    s = B.make_shape(T, D, N, Z, K, I, "bf16")
+    a = {k: flat(n - (k == name), dt) for k, (n, dt) in DISPATCH.items()}
+    with pytest.raises(ValueError, match=f"{name} has"):
+        B.permute_mxfp8_rows(s, *a.values(), flat(1024, U8))
+
+
+def w4_pair(rows, cols, group):
+    blocks = N * -(-rows // 16) * -(-cols // 128)
+    return flat(blocks * 1024, U8), flat(blocks * 2048 // group, BF16)
+
+
+@pytest.mark.parametrize("name,gather", [("x", True), ("x", False), ("offsets", True),
+                                         ("h", True), ("h", False)])
+def test_short_tensors_of_the_4bit_gate_up_are_refused(lib, name, gather):
+    s = B.make_shape(T, D, N, Z, K, I, "bf16")
+    n = {"x": (T if gather else R) * D, "offsets": N + 1, "h": R * I}
+    n[name] -= 1
+    with pytest.raises(ValueError, match=f"{name} has"):
+        B.expert_gate_up_w4(s, 64, flat(n["x"], BF16), flat(R, I32) if gather else None,
+                            w4_pair(I, D, 64), w4_pair(I, D, 64), flat(n["offsets"], I32),
+                            flat(n["h"], BF16), flat(1024, U8))
+
+
+@pytest.mark.parametrize("name", ["h", "offsets", "y_perm"])
+def test_short_tensors_of_the_4bit_down_are_refused(lib, name):
+    s = B.make_shape(T, D, N, Z, K, I, "bf16")
+    n = {"h": R * I, "offsets": N + 1, "y_perm": R * D}
+    n[name] -= 1
+    with pytest.raises(ValueError, match=f"{name} has"):
+        B.expert_down_w4(s, 64, flat(n["h"], BF16), w4_pair(D, I, 64), flat(n["offsets"], I32),
+                         flat(n["y_perm"], BF16), flat(1024, U8))
+
+
+def test_row_count_of_the_4bit_gate_up_stays_within_the_shape(lib):
+    s = B.make_shape(T, D, N, Z, K, I, "bf16")
+    for rows in (-1, R + 1):
+        code = lib.moe_expert_gate_up_w4_rows(ctypes.byref(s), 64, rows, FAKE, FAKE, FAKE, FAKE,
+                                              FAKE, FAKE, FAKE, FAKE, FAKE, 1 << 40, None)
+        assert code == 1 and b"n_rows" in lib.moe_last_error()
