@@ -481,12 +481,15 @@ def rmsnorm_backward(s, weight, inv_rms, dy, dx, dweight, ws, dsum=None, stream=
 class PreNormBuffers:
     """Buffers of the residual RMS norm in front of a layer, allocated once by torch:
     the sum, its norm y (the layer's x), the row factors, with mx the MXFP8 codes and
-    scales of y (forward_mxfp8's x_q), with train the gradients and their workspace."""
+    scales of y (forward_mxfp8's x_q), with train the gradients and their workspace.
+    normed: the rows that the last prenorm normed, which prenorm_backward reads: s, or
+    the caller's x of a call without a residual (to be left as it is until then)."""
 
     def __init__(self, shape: Shape, device="cuda", mx=False, train=False):
         T, d, dt = shape.T, shape.d, torch_dtype(shape)
         kw = dict(device=device)
         self.s = torch.empty((T, d), dtype=dt, **kw)
+        self.normed = self.s
         self.y = torch.empty((T, d), dtype=dt, **kw)
         self.inv_rms = torch.empty(T, dtype=torch.float32, **kw)
         self.x_q = (torch.empty((T, d), dtype=torch.uint8, **kw),
@@ -499,17 +502,20 @@ class PreNormBuffers:
 
 def prenorm(nb: PreNormBuffers, x, residual, weight, eps=1e-5, stream=None):
     """nb.s = x + residual and nb.y = its RMS norm times weight; returns nb.y, the x of
-    forward, forward_w4, forward_train or (with nb.x_q) forward_mxfp8."""
+    forward, forward_w4, forward_train or (with nb.x_q) forward_mxfp8.  residual None
+    (a model's first block): x itself is normed, nb.s is not written."""
     q, sf = nb.x_q if nb.x_q is not None else (None, None)
-    rmsnorm(x, weight, eps, nb.y, residual=residual, sum_out=nb.s, inv_rms=nb.inv_rms, y_q=q,
-            y_sf=sf, stream=stream)
+    rmsnorm(x, weight, eps, nb.y, residual=residual, sum_out=None if residual is None else nb.s,
+            inv_rms=nb.inv_rms, y_q=q, y_sf=sf, stream=stream)
+    nb.normed = x if residual is None else nb.s
     return nb.y
 
 
 def prenorm_backward(nb: PreNormBuffers, weight, dy, dsum=None, stream=None):
-    """Gradients of prenorm from dy (backward's dx) and dsum, the gradient that reaches
-    nb.s along the residual stream: nb.dx (of x and of residual) and nb.dweight."""
-    rmsnorm_backward(nb.s, weight, nb.inv_rms, dy, nb.dx, nb.dweight, nb.ws, dsum=dsum,
+    """Gradients of the last prenorm from dy (backward's dx) and dsum, the gradient that
+    reaches its sum along the residual stream: nb.dx (of x and of residual) and
+    nb.dweight."""
+    rmsnorm_backward(nb.normed, weight, nb.inv_rms, dy, nb.dx, nb.dweight, nb.ws, dsum=dsum,
                      stream=stream)
     return nb.dx
 

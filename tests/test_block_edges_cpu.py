@@ -72,3 +72,21 @@ def test_row_count_of_the_4bit_gate_up_stays_within_the_shape(lib):
         code = lib.moe_expert_gate_up_w4_rows(ctypes.byref(s), 64, rows, FAKE, FAKE, FAKE, FAKE,
                                               FAKE, FAKE, FAKE, FAKE, FAKE, 1 << 40, None)
         assert code == 1 and b"n_rows" in lib.moe_last_error()
+
+
+def test_prenorm_without_a_residual_norms_x_itself(lib, monkeypatch):
+    """A model's first block has no residual yet: no sum is asked for, and the backward pass
+    reads x, not a buffer that nothing wrote."""
+    calls = []
+    monkeypatch.setattr(B, "rmsnorm", lambda *a, **k: calls.append((a, k)))
+    monkeypatch.setattr(B, "rmsnorm_backward", lambda *a, **k: calls.append((a, k)))
+    nb = B.PreNormBuffers(B.make_shape(4, 64, 4, 2, 2, 64, "f32"), device="cpu", train=True)
+    x, r, w, dy = (torch.zeros((4, 64)) for _ in range(4))
+    B.prenorm(nb, x, None, w)
+    assert calls[-1][1]["residual"] is None and calls[-1][1]["sum_out"] is None
+    B.prenorm_backward(nb, w, dy)
+    assert calls[-1][0][0] is x
+    B.prenorm(nb, x, r, w)
+    assert calls[-1][1]["residual"] is r and calls[-1][1]["sum_out"] is nb.s
+    B.prenorm_backward(nb, w, dy)
+    assert calls[-1][0][0] is nb.s

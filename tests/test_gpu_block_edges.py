@@ -38,3 +38,38 @@ def test_w4_rows_behind_a_short_row_token_are_not_read(dtype, native, monkeypatc
         torch.cuda.synchronize()
         assert torch.equal(h[:rows], want[:rows]) and (h[rows:] == 7).all(), held
         assert B.device_status(ws) == (0 if held == R else B.DEV_BAD_OFFSETS), held
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prenorm_of_a_first_block(dtype):
+    """Without a residual prenorm is rmsnorm of x, and its backward pass that of x; the next
+    block's call with a residual on the same buffers is unchanged by it."""
+    shape = B.make_shape(9, 256, 4, 2, 2, 128, dtype)
+    dt = B.torch_dtype(shape)
+    g = torch.Generator().manual_seed(2)
+    x, r, dy = (torch.randn((9, 256), generator=g).to(dt).cuda() for _ in range(3))
+    w = (1 + 0.2 * torch.randn(256, generator=g)).to(dt).cuda()
+    mx = dtype == "bf16"
+    nb = B.PreNormBuffers(shape, mx=mx, train=True)
+    ws = B.new_rmsnorm_workspace(9, 256)
+    for res in (None, r, None):
+        nb.s.fill_(float("nan"))
+        y = B.prenorm(nb, x, res, w)
+        B.prenorm_backward(nb, w, dy, dsum=r)
+        s = x if res is None else torch.empty_like(x)
+        y2, inv = torch.empty_like(x), torch.empty(9, device="cuda")
+        q, sf = (torch.empty_like(t) for t in nb.x_q) if mx else (None, None)
+        B.rmsnorm(x, w, 1e-5, y2, residual=res, sum_out=None if res is None else s, inv_rms=inv,
+                  y_q=q, y_sf=sf)
+        dx, dw = torch.empty_like(x), torch.empty_like(w)
+        B.rmsnorm_backward(s, w, inv, dy, dx, dw, ws, dsum=r)
+        torch.cuda.synchronize()
+        assert torch.equal(y, y2) and torch.equal(nb.inv_rms, inv)
+        assert torch.equal(nb.dx, dx) and torch.equal(nb.dweight, dw)
+        if mx:
+            assert torch.equal(nb.x_q[0], q) and torch.equal(nb.x_q[1], sf)
+        s64 = s.double()
+        want = s64 * (s64.square().mean(1, keepdim=True) + 1e-5).rsqrt() * w.double()
+        # fp32 arithmetic (a sum of 256, its root, two products) and one rounding of the type
+        tol = want.abs() * (torch.finfo(dt).eps / 2 + 24 * 2.0 ** -24)
+        assert ((y.double() - want).abs() <= tol * (1 + 2.0 ** -7)).all()
