@@ -611,6 +611,14 @@ def clip_gradients(grads: GradientList, max_norm, norm, stream=None):
     return norm
 
 
+def clip_by_norm(grads: GradientList, max_norm, norm, stream=None):
+    """The second half of clip_gradients, by a norm that is at hand: gradient_norm's, or
+    that of several ranks (the root of the sum of their norms' squares)."""
+    n, table, np, _ = _norm_args(grads, norm)
+    _check(lib().moe_grad_clip(n, table, float(max_norm), np, _stream(stream)))
+    return norm
+
+
 def workspace_bytes(shape: Shape) -> int:
     n = lib().moe_workspace_bytes(ctypes.byref(shape))
     if n == 0:

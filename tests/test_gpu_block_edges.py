@@ -73,3 +73,32 @@ def test_prenorm_of_a_first_block(dtype):
         # fp32 arithmetic (a sum of 256, its root, two products) and one rounding of the type
         tol = want.abs() * (torch.finfo(dt).eps / 2 + 24 * 2.0 ** -24)
         assert ((y.double() - want).abs() <= tol * (1 + 2.0 ** -7)).all()
+
+
+def test_clip_by_a_joined_norm():
+    """Two ranks' lists, each clipped by the norm of both, are one list clipped by its own: the
+    factor's rounding (3 * 2^-24), the norm's (6 * 2^-24 on each side) and the result's."""
+    g = torch.Generator().manual_seed(3)
+    lists = [[(torch.randn(n, generator=g) * 0.1).to(dt).cuda() for n, dt in spec]
+             for spec in (((1001, torch.float32), (70_000, torch.bfloat16)),
+                          ((5, torch.bfloat16), (33_333, torch.float32)))]
+    before = [[t.clone() for t in ts] for ts in lists]
+    norms = [torch.empty(1, device="cuda") for _ in lists]
+    plans = [B.GradientList(ts) for ts in lists]
+    for p, n in zip(plans, norms):
+        B.gradient_norm(p, n)
+    joined = (norms[0].double().square() + norms[1].double().square()).sqrt().float()
+    for p in plans:
+        assert B.clip_by_norm(p, 0.5, joined) is joined
+    torch.cuda.synchronize()
+    n64 = sum(float(t.double().square().sum()) for ts in before for t in ts) ** 0.5
+    assert abs(float(joined) - n64) <= 7 * 2.0 ** -24 * n64
+    for ts, old in zip(lists, before):
+        for a, b in zip(ts, old):
+            w = b.double() * (0.5 / (n64 + 1e-6))
+            tol = w.abs() * (torch.finfo(a.dtype).eps / 2 + 16 * 2.0 ** -24) * (1 + 2.0 ** -7)
+            assert ((a.double() - w).abs() <= tol + 1e-38).all()
+    with pytest.raises(B.MoEError, match="max_norm"):
+        B.clip_by_norm(plans[0], -1.0, joined)
+    with pytest.raises(ValueError, match="norm has 2 elements"):
+        B.clip_by_norm(plans[0], 1.0, torch.empty(2, device="cuda"))
