@@ -529,10 +529,25 @@ class _Grad(ctypes.Structure):
                 ("dtype", ctypes.c_int32)]
 
 
+def _finish(stream=None):
+    """Waits for `stream` (None: the current one), so that what it did holds for every
+    other.  A capture is left alone: it may not wait, and orders its own nodes."""
+    stream = torch.cuda.current_stream() if stream is None else stream
+    if torch.cuda.is_current_stream_capturing():
+        return
+    with torch.cuda.stream(stream):
+        capturing = torch.cuda.is_current_stream_capturing()
+    if not capturing:
+        stream.synchronize()
+
+
 class GradientList:
     """Gradient tensors (fp32 or bf16, contiguous, on one device) taken as one vector,
     with the workspace of their norm.  out: where the clipped gradients go (by
-    default in place).  The list holds the tensors; make a new one when they change."""
+    default in place).  The list holds the tensors; make a new one when they change.
+    It may be used on any stream, by one call at a time (its calls share the workspace:
+    put those of several streams in order).  Made while a stream is captured, it belongs
+    to that graph."""
 
     def __init__(self, tensors, out=None, stream=None):
         self.tensors = list(tensors)
@@ -560,6 +575,7 @@ class GradientList:
         self.ws = torch.empty(ws_bytes, dtype=torch.uint8, device=self.device)
         _here(self.ws)
         _check(lib().moe_workspace_init(_p(self.ws), ws_bytes, _stream(stream)))
+        _finish(stream)
 
     def _check_overlap(self):
         """Every element is written once, and only from its own gradient."""

@@ -102,3 +102,43 @@ def test_clip_by_a_joined_norm():
         B.clip_by_norm(plans[0], -1.0, joined)
     with pytest.raises(ValueError, match="norm has 2 elements"):
         B.clip_by_norm(plans[0], 1.0, torch.empty(2, device="cuda"))
+
+
+def test_a_gradient_list_is_ready_for_any_stream():
+    """Made on a stream that is busy, used at once on another: the workspace is clear by then
+    (its memory held ones before)."""
+    n = B.lib().moe_grad_workspace_bytes(1)
+    g = torch.linspace(-1, 1, 4097, device="cuda")
+    want = float(g.double().norm())
+    busy, other = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for explicit in (False, True):
+        norm = torch.zeros(1, device="cuda")
+        with torch.cuda.stream(busy):
+            torch.full((n,), 0xff, dtype=torch.uint8, device="cuda")  # freed, taken again below
+            torch.cuda._sleep(20_000_000)
+            if not explicit:
+                plan = B.GradientList([g])
+        if explicit:
+            plan = B.GradientList([g], stream=busy)
+        B.gradient_norm(plan, norm, stream=other)
+        torch.cuda.synchronize()
+        assert abs(float(norm) - want) <= 6 * 2.0 ** -24 * want
+
+
+def test_a_gradient_list_made_in_a_capture():
+    """Its clearing becomes part of the graph, in front of the calls on it."""
+    g = torch.linspace(-1, 1, 4097, device="cuda")
+    norm = torch.zeros(1, device="cuda")
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        plan = B.GradientList([g])
+        B.gradient_norm(plan, norm)
+    for scale in (1.0, 2.0):
+        g.mul_(scale)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = float(g.double().norm())
+        assert abs(float(norm) - want) <= 6 * 2.0 ** -24 * want
+    del plan, graph
