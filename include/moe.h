@@ -503,7 +503,7 @@ typedef struct {
 } moe_grad;
 
 /* Bytes of device workspace for a list of n_tensors (0 for a negative n).  Clear
- * it once with moe_workspace_init. */
+ * it once with moe_workspace_init; it serves one call at a time, in stream order. */
 size_t moe_grad_workspace_bytes(int32_t n_tensors);
 
 /* *norm = sqrt(sum of g^2 over every element of every tensor), fp32 on the

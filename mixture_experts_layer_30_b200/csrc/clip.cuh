@@ -121,7 +121,9 @@ grad_norm_kernel(const __grid_constant__ ClipTable tab, double* part, int base, 
   if (threadIdx.x == 0) {
     part[base + blockIdx.x] = sum;
     __threadfence();
-    last = norm && atomicAdd(ticket, 1u) == gridDim.x - 1;
+    // wraps to 0 by itself: it is ready for the next call on this workspace, also where two
+    // ran at once
+    last = norm && atomicInc(ticket, gridDim.x - 1) == gridDim.x - 1;
   }
   __syncthreads();
   if (!last) return;
@@ -129,10 +131,7 @@ grad_norm_kernel(const __grid_constant__ ClipTable tab, double* part, int base, 
   double t = 0.0;
   for (int j = threadIdx.x; j < total_parts; j += kClipThreads) t += __ldcg(part + j);
   t = block_sum(t);
-  if (threadIdx.x == 0) {
-    *norm = (float)sqrt(t);
-    *ticket = 0;  // ready for the next call on this workspace
-  }
+  if (threadIdx.x == 0) *norm = (float)sqrt(t);
 }
 
 template <typename T>

@@ -142,3 +142,21 @@ def test_a_gradient_list_made_in_a_capture():
         want = float(g.double().norm())
         assert abs(float(norm) - want) <= 6 * 2.0 ** -24 * want
     del plan, graph
+
+
+def test_a_norm_after_two_at_once_is_right():
+    """Two calls of one list in flight at once are not promised a norm, but they leave the
+    workspace as they found it."""
+    ts = [torch.full((3_000_001,), 0.5, device="cuda"), torch.full((77,), 2.0, device="cuda")]
+    plan = B.GradientList(ts)
+    want = (3_000_001 * 0.25 + 77 * 4.0) ** 0.5
+    streams, norms = [torch.cuda.Stream() for _ in range(2)], torch.zeros(3, 1, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for st, n in zip(streams, norms):
+            B.gradient_norm(plan, n, stream=st)
+        torch.cuda.synchronize()
+        norms[2].zero_()
+        B.gradient_norm(plan, norms[2])
+        assert abs(float(norms[2]) - want) <= 6 * 2.0 ** -24 * want
+        assert int(plan.ws[4:8].view(torch.int32)) == 0
