@@ -507,8 +507,9 @@ typedef struct {
 size_t moe_grad_workspace_bytes(int32_t n_tensors);
 
 /* *norm = sqrt(sum of g^2 over every element of every tensor), fp32 on the
- * device; 0 for an empty list.  Squares are formed in fp32 (entries above 1.8e19
- * in magnitude make the norm infinite) and summed in fp64, in a fixed order. */
+ * device; 0 for an empty list.  The squares of 16 bytes are formed and added in fp32
+ * (scaled where they would leave its range), their sums in fp64, in a fixed order: the
+ * norm is infinite only for an infinite entry or past fp32's largest number. */
 moe_status moe_grad_norm(int32_t n_tensors, const moe_grad* list, float* norm, void* ws,
                          size_t ws_bytes, void* stream);
 

@@ -160,3 +160,52 @@ def test_a_norm_after_two_at_once_is_right():
         B.gradient_norm(plan, norms[2])
         assert abs(float(norms[2]) - want) <= 6 * 2.0 ** -24 * want
         assert int(plan.ws[4:8].view(torch.int32)) == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("scale", [1e-37, 1e-30, 1e-22, 3e-23, 2e-23, 1e-19, 1e-16, 1e16, 1e19,
+                                   1e20, 1e30])
+def test_norm_of_gradients_whose_squares_leave_fp32(scale, dtype):
+    """Below 1e-19 the squares lose their bits in fp32, above 1.8e19 they are infinite.  In 64 bits
+    every square of such a vector is exact; where the sum of 4 or 8 is formed in fp32 it is at
+    least 2^-110, so that a square below the normal range adds at most 2^-149: the bound of the
+    other sizes holds."""
+    g = torch.Generator().manual_seed(4)
+    for n in (1, 5, 8, 8191, 100_003):
+        base = (torch.randn(n + 3, generator=g) * scale).to(dtype).cuda()
+        for start in (0, 3):
+            t = base[start:start + n]
+            norm = torch.zeros(1, device="cuda")
+            B.gradient_norm(B.GradientList([t]), norm)
+            want = float(t.double().square().sum().sqrt())
+            assert 0 < want < 3.4e38
+            assert abs(float(norm) - want) <= 6 * 2.0 ** -24 * want + 2.0 ** -150
+
+
+def test_one_large_entry_leaves_the_other_gradients():
+    """A finite entry above 1.8e19 has a finite norm: the factor is small, not 0."""
+    g = torch.full((1000,), 1e15, device="cuda")
+    g[17] = 1e20
+    keep = g.double()
+    norm = torch.zeros(1, device="cuda")
+    B.clip_gradients(B.GradientList([g]), 1.0, norm)
+    want = float(keep.norm())
+    assert abs(float(norm) - want) <= 6 * 2.0 ** -24 * want
+    w = keep / want
+    assert ((g.double() - w).abs() <= w * (13 * 2.0 ** -24) * (1 + 2.0 ** -7)).all()
+
+
+def test_norm_of_ordinary_and_extreme_entries_together():
+    """Small entries beside an ordinary one in the same vector, zeros, and a norm below fp32's
+    smallest normal number."""
+    t = torch.zeros(4096, device="cuda")
+    t[0], t[1], t[4000] = 3.0, 1e-25, 1e-25
+    norm = torch.zeros(1, device="cuda")
+    B.gradient_norm(B.GradientList([t]), norm)
+    assert float(norm) == 3.0
+    t.zero_()
+    B.gradient_norm(B.GradientList([t]), norm)
+    assert float(norm) == 0.0
+    t[7] = 2.0 ** -140
+    B.gradient_norm(B.GradientList([t]), norm)
+    assert float(norm) == 2.0 ** -140
