@@ -481,8 +481,8 @@ size_t moe_rmsnorm_workspace_bytes(int32_t T, int32_t d);
  *   dx = inv_rms * (weight * dy - xhat * mean_j(weight * dy * xhat)) + dsum
  *   dweight[j] = sum_t dy[t, j] * xhat[t, j]
  * dx is the gradient of x and of residual.  s is sum_out of the forward call (x
- * without a residual), inv_rms its output.  Sums are fp32 in a fixed order (the
- * last of an fp32 dweight fp64); dx [T, d] and dweight [d] have the dtype and are
+ * without a residual), inv_rms its output.  Sums are fp32 in a fixed order (an fp32
+ * dweight's over the CTAs fp64); dx [T, d] and dweight [d] have the dtype and are
  * rounded once.  dx may be dy or dsum.  With T == 0 dweight is set to zero. */
 moe_status moe_rmsnorm_backward(int32_t T, int32_t d, int32_t dtype, const void* s,
                                 const void* weight, const float* inv_rms, const void* dy,

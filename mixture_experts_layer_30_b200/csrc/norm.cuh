@@ -352,25 +352,27 @@ rmsnorm_bwd_kernel(const T* s, const T* __restrict__ w, const float* __restrict_
 }
 
 // dw[j] = sum over the n partial rows in a fixed order: 32 columns a CTA, 32
-// warps that each sum every 32nd row, joined by one warp a column: in fp64 for an fp32
-// dw (333 x 1000: error against 64 bits 7.5e-8 of the norm, 1.3e-7 with a join in fp32).
-// n = 0 gives 0.
+// warps that each sum every 32nd row, joined by one warp a column.  An fp32 dw is summed
+// in fp64: its error against 64 bits is 5.2e-8 of its norm at 333 x 1000 and 6.7e-8 at
+// 4096 x 2048 (7.0e-8 and 1.0e-7 with the warps' sums in fp32), the time 5.78 against 5.75 us.
+// A bf16 one gains nothing by it and stays in fp32.  n = 0 gives 0.
 template <typename T>
 __global__ void __launch_bounds__(1024)
 rmsnorm_dw_kernel(const float* __restrict__ part, int n, int d, T* __restrict__ dw) {
   pdl_trigger();
   pdl_wait();
-  __shared__ float acc[32][33];
+  using Sum = std::conditional_t<sizeof(T) == 4, double, float>;
+  __shared__ Sum acc[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int j = blockIdx.x * 32 + lane, mine = blockIdx.x * 32 + warp;
-  float v = 0.f;
+  Sum v = 0;
   if (j < d) {
 #pragma unroll 8
     for (int r = warp; r < n; r += 32) v += part[(size_t)r * d + j];
   }
   acc[warp][lane] = v;
   __syncthreads();
-  std::conditional_t<sizeof(T) == 4, double, float> t = acc[lane][warp];
+  Sum t = acc[lane][warp];
 #pragma unroll
   for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
   if (lane == 0 && mine < d) dw[mine] = Cvt<T>::from_f((float)t);

@@ -209,3 +209,25 @@ def test_norm_of_ordinary_and_extreme_entries_together():
     t[7] = 2.0 ** -140
     B.gradient_norm(B.GradientList([t]), norm)
     assert float(norm) == 2.0 ** -140
+
+
+@pytest.mark.parametrize("T", [592, 1184, 4000])
+def test_fp32_weight_gradient_keeps_small_rows(T):
+    """s = weight = inv_rms = 1, so a column's terms are dy itself: 1 in the first 32 rows, then
+    2^-25, which an fp32 sum of ones drops.  A CTA's own rows are summed in fp32, exactly here:
+    a CTA has at most 7 of them, at a stride of the grid, so all but 32 CTAs sum small terms
+    alone and those 32 lose at most 6 * 2^-25 each.  The join of the CTAs is fp64 and the result is
+    rounded once: 2^-24 of it."""
+    d = 2048
+    one = torch.ones((T, d), device="cuda")
+    dy = torch.full((T, d), 2.0 ** -25, device="cuda")
+    dy[:32] = 1.0
+    dw, dx = torch.empty(d, device="cuda"), torch.empty_like(one)
+    B.rmsnorm_backward(one, one[0].clone(), torch.ones(T, device="cuda"), dy, dx, dw,
+                       B.new_rmsnorm_workspace(T, d))
+    torch.cuda.synchronize()
+    want = 32 + (T - 32) * 2.0 ** -25
+    per = -(-T // 592)
+    tol = want * 2.0 ** -24 + 32 * (per - 1) * 2.0 ** -25
+    assert (T - 32) * 2.0 ** -25 > 2 * tol  # an fp32 join would be seen
+    assert float((dw.double() - want).abs().max()) <= tol
