@@ -3,7 +3,8 @@
     python -m mixture_experts_layer_30_b200.build
 
 One object per translation unit, compiled in parallel; an object is compiled
-again when a file that it includes is newer.
+again when a file that it includes is newer, the native module also when torch or
+Python is another one.
 """
 import os
 import shutil
@@ -18,6 +19,7 @@ OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_b200.so")
 CALLS = os.path.join(PKG, "_calls.so")
 CALLS_SRC = os.path.join(CSRC, "calls.cpp")
+CALLS_FOR = os.path.join(OBJ, "_calls.for")  # the torch and Python that CALLS was built for
 SOURCES = [os.path.join(CSRC, "moe_api.cu"), os.path.join(CSRC, "block_api.cu")]
 
 
@@ -51,6 +53,20 @@ def _stale(obj: str) -> bool:
                for n in names + [os.path.abspath(__file__)])
 
 
+def _calls_tag() -> str:
+    import torch
+    return (f"torch {torch.__version__}, C++11 ABI {int(torch._C._GLIBCXX_USE_CXX11_ABI)}, "
+            f"{sysconfig.get_config_var('SOABI')}")
+
+
+def _calls_match() -> bool:
+    """Whether _calls.so was built for this torch and Python."""
+    if not os.path.exists(CALLS_FOR):
+        return False
+    with open(CALLS_FOR) as f:
+        return f.read() == _calls_tag()
+
+
 def _calls_commands():
     """Compile and link commands of _calls.so: a CPython module on torch's tensors that
     calls libmoe_b200.so beside it."""
@@ -74,8 +90,10 @@ def _calls_commands():
 
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
     newest = _newest_input_mtime()
-    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= newest
-                         for f in (LIB, CALLS)):
+    lib_fresh, calls_fresh = (not force and os.path.exists(f) and os.path.getmtime(f) >= newest
+                              for f in (LIB, CALLS))
+    same_torch = _calls_match()
+    if lib_fresh and calls_fresh and same_torch:
         return LIB
     os.makedirs(OBJ, exist_ok=True)
     base = [nvcc_path(), "-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo",
@@ -84,14 +102,14 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
     if ptxas_verbose:
         base[1:1] = ["-Xptxas", "-v"]
     runs = []
-    for src in SOURCES:
+    for src in [] if lib_fresh else SOURCES:
         obj = _object_of(src)
         if force or _stale(obj):
             cmd = base + ["-MD", "-MF", obj + ".d", "-c", src, "-o", obj + ".tmp"]
             runs.append((obj, subprocess.Popen(cmd, stdout=subprocess.PIPE,
                                                stderr=subprocess.STDOUT, text=True)))
     calls_obj, calls_compile, calls_link = _calls_commands()
-    if force or _stale(calls_obj):
+    if force or not same_torch or _stale(calls_obj):
         runs.append((calls_obj, subprocess.Popen(calls_compile, stdout=subprocess.PIPE,
                                                  stderr=subprocess.STDOUT, text=True)))
     failed = ""
@@ -106,12 +124,15 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
     if failed:
         raise RuntimeError("compilation failed:\n" + failed)
     soname = ["-Xlinker", "-soname=" + os.path.basename(LIB)]
-    for out, cmd in ((LIB, base + ["-shared", "-o", LIB + ".tmp"] + soname
-                      + [_object_of(s) for s in SOURCES]), (CALLS, calls_link)):
+    links = [(LIB, base + ["-shared", "-o", LIB + ".tmp"] + soname
+              + [_object_of(s) for s in SOURCES]), (CALLS, calls_link)]
+    for out, cmd in links[1:] if lib_fresh else links:
         res = subprocess.run(cmd, capture_output=True, text=True)
         if res.returncode != 0:
             raise RuntimeError("link failed:\n" + (res.stdout + res.stderr)[-4000:])
         os.replace(out + ".tmp", out)
+    with open(CALLS_FOR, "w") as f:
+        f.write(_calls_tag())
     return LIB
 
 

@@ -90,3 +90,26 @@ def test_prenorm_without_a_residual_norms_x_itself(lib, monkeypatch):
     assert calls[-1][1]["residual"] is r and calls[-1][1]["sum_out"] is nb.s
     B.prenorm_backward(nb, w, dy)
     assert calls[-1][0][0] is nb.s
+
+
+class _Compiled(Exception):
+    pass
+
+
+def test_native_module_of_another_torch_is_built_again(lib, monkeypatch):
+    """It uses torch's C++ interface: one compiled against another version is not fresh,
+    however new its file is; the CUDA library does not depend on torch and stays."""
+    commands = []
+
+    def record(cmd, **kw):
+        commands.append(cmd)
+        raise _Compiled
+    monkeypatch.setattr(BUILD.subprocess, "Popen", record)
+    monkeypatch.setattr(BUILD.subprocess, "run", record)
+    BUILD.build()
+    assert not commands
+    monkeypatch.setattr(torch, "__version__", "0.0.0")
+    with pytest.raises(_Compiled):
+        BUILD.build()
+    assert [c for c in commands if BUILD.CALLS_SRC in c] and not [c for c in commands
+                                                                  if BUILD.SOURCES[0] in c]
