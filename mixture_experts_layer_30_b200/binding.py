@@ -7,6 +7,7 @@ the library is missing, every call raises.
 """
 import ctypes
 import os
+import warnings
 
 import torch
 
@@ -117,12 +118,25 @@ def lib():
     return _lib
 
 
+class _NotNative:
+    """In place of a native module that cannot be loaded: takes no call."""
+
+    def __getattr__(self, name):
+        return lambda *args: -1
+
+
 def _native():
-    """The module of the short calls (raises if it was not built)."""
+    """The module of the short calls; without it they take the checked path behind it.
+    The CUDA library has to be there either way."""
     global _calls
     if _calls is None:
         lib()
-        from . import _calls as module
+        try:
+            from . import _calls as module
+        except ImportError as e:
+            warnings.warn(f"the native module _calls is not used, calls take a few microseconds "
+                          f"more on the host: {e}", RuntimeWarning, stacklevel=3)
+            module = _NotNative()
         _calls = module
     return _calls
 

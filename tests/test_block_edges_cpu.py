@@ -113,3 +113,24 @@ def test_native_module_of_another_torch_is_built_again(lib, monkeypatch):
         BUILD.build()
     assert [c for c in commands if BUILD.CALLS_SRC in c] and not [c for c in commands
                                                                   if BUILD.SOURCES[0] in c]
+
+
+def test_calls_go_on_without_the_native_module(lib, monkeypatch):
+    """It only shortens the host's part: where it cannot be loaded, the binding's checked path
+    makes the same calls, with a warning.  The CUDA library itself has no stand-in."""
+    import sys
+
+    import mixture_experts_layer_30_b200 as package
+    monkeypatch.delattr(package, "_calls", raising=False)
+    monkeypatch.setitem(sys.modules, package.__name__ + "._calls", None)
+    monkeypatch.setattr(B, "_calls", None)
+    s = B.make_shape(T, D, N, Z, K, I, "bf16")
+    with pytest.warns(RuntimeWarning, match="_calls"):
+        with pytest.raises(ValueError, match="y_perm has"):
+            B.expert_down_w4(s, 64, flat(R * I, BF16), w4_pair(D, I, 64), flat(N + 1, I32),
+                             flat(R * D - 1, BF16), flat(1024, U8))
+    monkeypatch.setattr(B, "_lib", None)
+    monkeypatch.setattr(B, "_calls", None)
+    monkeypatch.setattr(B, "LIB_PATH", "/nowhere/libmoe_b200.so")
+    with pytest.raises(RuntimeError, match="missing"):
+        B._native()
