@@ -284,7 +284,7 @@ moe_status moe_expert_down_mxfp8(const moe_shape* shape, const void* h_q, const 
  * of it column 2 p (p < 4) or 2 (p - 4) + 1 of those eight.  Scales:
  * [matrix, row block, column block, 16, 128 / group].  The shape's weight_layout
  * is ignored.  Row lengths d and I must be multiples of 16 bytes (8 bf16 or 4
- * fp32 values), T * K at most 2^31 - 65. */
+ * fp32 values), T * K at most 2^31 - 65, d and I at most 2^31 - 129. */
 
 /* Bytes of the codes and of the scales of n_mats matrices [rows, cols] (0 for
  * invalid arguments). */

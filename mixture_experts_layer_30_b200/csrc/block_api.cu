@@ -306,7 +306,7 @@ moe_status w4_product(const moe_shape& s, const W4Args& a) {
 }
 
 // I is the contraction of the second half: its rows are read 16 bytes at a time.  A chunk's
-// end is a 32-bit row number, up to kW4Tile behind the last row.
+// end is a 32-bit row number, up to kW4Tile behind the last row, and a block's a 32-bit column.
 moe_status check_w4_shape(const moe_shape& s) {
   const int vec = s.dtype == MOE_BF16 ? 8 : 4;
   if (s.I % vec)
@@ -314,6 +314,8 @@ moe_status check_w4_shape(const moe_shape& s) {
   if ((long long)s.T * s.K > 0x7fffffffLL - moe::kW4Tile)
     return fail(MOE_ERR_UNSUPPORTED, "T*K=%lld routed rows leave a chunk's end past int32",
                 (long long)s.T * s.K);
+  if (std::max(s.d, s.I) > INT32_MAX - moe::kW4Cols)
+    return fail(MOE_ERR_UNSUPPORTED, "d=%d, I=%d leave a block's end past int32", s.d, s.I);
   return MOE_OK;
 }
 

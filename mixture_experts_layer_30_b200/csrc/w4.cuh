@@ -24,8 +24,9 @@ namespace moe {
 
 constexpr int kW4Rows = 16, kW4Cols = 128, kW4Block = 1024;  // one block of codes, bytes
 
-__host__ MOE_DEV int w4_row_blocks(int rows) { return (rows + kW4Rows - 1) / kW4Rows; }
-__host__ MOE_DEV int w4_col_blocks(int cols) { return (cols + kW4Cols - 1) / kW4Cols; }
+// unsigned: the rounding up of a size next to 2^31
+__host__ MOE_DEV int w4_row_blocks(int rows) { return ((unsigned)rows + kW4Rows - 1) / kW4Rows; }
+__host__ MOE_DEV int w4_col_blocks(int cols) { return ((unsigned)cols + kW4Cols - 1) / kW4Cols; }
 
 // One CTA per block; a thread takes eight columns of one row.  scale =
 // round_bf16(amax / 7), code = 8 + round(w / scale) (nearest even, 0 where the

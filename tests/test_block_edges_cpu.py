@@ -134,3 +134,17 @@ def test_calls_go_on_without_the_native_module(lib, monkeypatch):
     monkeypatch.setattr(B, "LIB_PATH", "/nowhere/libmoe_b200.so")
     with pytest.raises(RuntimeError, match="missing"):
         B._native()
+
+
+def test_w4_sizes_next_to_32_bits(lib):
+    assert lib.moe_w4_code_bytes(1, 2 ** 31 - 1, 1) == 2 ** 27 * 1024
+    assert lib.moe_w4_code_bytes(1, 1, 2 ** 31 - 1) == 2 ** 24 * 1024
+    assert lib.moe_w4_scale_bytes(1, 2 ** 31 - 1, 1, 128) == 2 ** 27 * 32
+    # the end of the last block of columns would not be a 32-bit number
+    for d, I in ((2 ** 31 - 8, 8), (8, 2 ** 31 - 8)):
+        s = B.make_shape(1, d, 1, 0, 1, I, "bf16")
+        for code in (lib.moe_expert_gate_up_w4(ctypes.byref(s), 32, FAKE, FAKE, FAKE, FAKE, FAKE,
+                                               FAKE, FAKE, FAKE, FAKE, 1 << 60, None),
+                     lib.moe_expert_down_w4(ctypes.byref(s), 32, FAKE, FAKE, FAKE, FAKE, FAKE,
+                                            FAKE, 1 << 60, None)):
+            assert code == 2 and b"past int32" in lib.moe_last_error()
