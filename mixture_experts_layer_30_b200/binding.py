@@ -360,6 +360,8 @@ def quantize_weights_w4(w: torch.Tensor, group: int = 128, stream=None):
     n, rows, cols = w.shape
     if w.dtype not in _DTYPE_CODES:
         raise ValueError(f"w has dtype {w.dtype}, expected torch.float32 or torch.bfloat16")
+    if max(w.shape) > 0x7fffffff:  # ctypes would cut it to 32 bits
+        raise ValueError(f"w {tuple(w.shape)}: more than 2^31 - 1 matrices, rows or columns")
     if group not in (32, 64, 128):
         raise MoEError(2, f"group {group} is none of 32, 64, 128")
     _here(w)

@@ -148,3 +148,10 @@ def test_w4_sizes_next_to_32_bits(lib):
                      lib.moe_expert_down_w4(ctypes.byref(s), 32, FAKE, FAKE, FAKE, FAKE, FAKE,
                                             FAKE, 1 << 60, None)):
             assert code == 2 and b"past int32" in lib.moe_last_error()
+
+
+@pytest.mark.parametrize("shape", [(2 ** 31, 1, 1), (1, 2 ** 32 + 16, 1), (1, 1, 2 ** 31)])
+def test_4bit_weights_past_32_bits_are_refused(lib, shape):
+    """As 32-bit numbers these would be negative or another, small size."""
+    with pytest.raises(ValueError, match="more than"):
+        B.quantize_weights_w4(torch.empty(shape, dtype=BF16, device="meta"))
