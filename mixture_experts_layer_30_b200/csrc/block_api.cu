@@ -127,12 +127,11 @@ struct NormArgs {
 };
 
 template <typename T, int VPT, bool kRes, bool kMx>
-cudaError_t norm_launch(const NormArgs& a, int threads, int rows_per_cta) {
-  const unsigned grid = (unsigned)((a.T + (long long)rows_per_cta - 1) / rows_per_cta);
-  return moe::launch_pdl(moe::rmsnorm_kernel<T, VPT, kRes, kMx>, dim3(grid),
-                         dim3(threads, rows_per_cta), 0, a.st, static_cast<const T*>(a.x),
-                         static_cast<const T*>(a.res), static_cast<const T*>(a.w), a.eps, a.T, a.d,
-                         static_cast<T*>(a.sum), static_cast<T*>(a.y), a.inv, a.yq, a.ysf);
+cudaError_t norm_launch(const NormArgs& a, int threads) {
+  return moe::launch_pdl(moe::rmsnorm_kernel<T, VPT, kRes, kMx>, dim3(a.T), dim3(threads), 0, a.st,
+                         static_cast<const T*>(a.x), static_cast<const T*>(a.res),
+                         static_cast<const T*>(a.w), a.eps, a.d, static_cast<T*>(a.sum),
+                         static_cast<T*>(a.y), a.inv, a.yq, a.ysf);
 }
 
 template <typename T, bool kRes, bool kMx>
@@ -140,10 +139,10 @@ cudaError_t norm_dispatch(const NormArgs& a) {
   const int nvec = a.d / moe::Vec16<T>::kN;
   // threads of one row for vpt vectors each, a whole number of warps
   auto width = [&](int vpt) { return ((nvec + vpt - 1) / vpt + 31) / 32 * 32; };
-  if (width(1) <= 256) return norm_launch<T, 1, kRes, kMx>(a, width(1), 1);
-  if (width(2) <= 256) return norm_launch<T, 2, kRes, kMx>(a, width(2), 1);
-  if (width(4) <= 1024) return norm_launch<T, 4, kRes, kMx>(a, width(4), 1);
-  return norm_launch<T, 0, kRes, kMx>(a, 1024, 1);
+  if (width(1) <= 256) return norm_launch<T, 1, kRes, kMx>(a, width(1));
+  if (width(2) <= 256) return norm_launch<T, 2, kRes, kMx>(a, width(2));
+  if (width(4) <= 1024) return norm_launch<T, 4, kRes, kMx>(a, width(4));
+  return norm_launch<T, 0, kRes, kMx>(a, 1024);
 }
 
 template <typename T>

@@ -77,22 +77,19 @@ MOE_DEV void norm_emit(const float* f, float inv, const uint4& wraw, bool active
   }
 }
 
-// One row per blockDim.x threads, blockDim.y rows a CTA; VPT vectors of a row
-// per thread in registers, or VPT = 0: rows longer than the registers hold are
-// read a second time (from the stored sum when there is a residual).  Outputs
-// may share memory with inputs of the same row: a thread reads its vectors
-// before it writes them.
+// One row a CTA; VPT vectors of it per thread in registers, or VPT = 0: rows longer
+// than the registers hold are read a second time (from the stored sum when there is
+// a residual).  Outputs may share memory with inputs of the same row: a thread reads
+// its vectors before it writes them.
 template <typename T, int VPT, bool kRes, bool kMx>
 __global__ void __launch_bounds__(1024)
-rmsnorm_kernel(const T* x, const T* res, const T* __restrict__ w, float eps, int rows, int d,
-               T* sum_out, T* y, float* inv_out, uint8_t* yq, uint8_t* ysf) {
+rmsnorm_kernel(const T* x, const T* res, const T* __restrict__ w, float eps, int d, T* sum_out,
+               T* y, float* inv_out, uint8_t* yq, uint8_t* ysf) {
   pdl_trigger();
   pdl_wait();
   constexpr int VN = Vec16<T>::kN;
-  __shared__ float red[32 * 4];
-  const int row_i = blockIdx.x * blockDim.y + threadIdx.y;
-  const bool live = row_i < rows;
-  const size_t row = live ? row_i : 0;
+  __shared__ float red[32];
+  const size_t row = blockIdx.x;
   const int nvec = d / VN, tid = threadIdx.x, step = blockDim.x;
   const uint4* xv = reinterpret_cast<const uint4*>(x + row * d);
   const uint4* rv = kRes ? reinterpret_cast<const uint4*>(res + row * d) : nullptr;
@@ -123,7 +120,7 @@ rmsnorm_kernel(const T* x, const T* res, const T* __restrict__ w, float eps, int
       const int v = tid + i * step;
       a[i] = make_uint4(0, 0, 0, 0);
       b[i] = wr[i] = a[i];
-      if (live && v < nvec) {
+      if (v < nvec) {
         a[i] = xv[v];
         if constexpr (kRes) b[i] = rv[v];
         wr[i] = __ldg(wv + v);
@@ -133,31 +130,31 @@ rmsnorm_kernel(const T* x, const T* res, const T* __restrict__ w, float eps, int
     for (int i = 0; i < VPT; ++i) {
       const int v = tid + i * step;
       float f[VN];
-      if (live && v < nvec) a[i] = take(a[i], b[i], v, f);
+      if (v < nvec) a[i] = take(a[i], b[i], v, f);
     }
-    ss = row_sum(ss, red + 32 * threadIdx.y);
+    ss = row_sum(ss, red);
     const float inv = 1.0f / sqrtf(ss / (float)d + eps);
-    if (live && tid == 0 && inv_out) inv_out[row] = inv;
+    if (tid == 0 && inv_out) inv_out[row] = inv;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = tid + i * step;
       float f[VN];
       unpack16(a[i], f, T());
-      norm_emit<T, kMx>(f, inv, wr[i], live && v < nvec, v, row, d, y, yq, ysf);
+      norm_emit<T, kMx>(f, inv, wr[i], v < nvec, v, row, d, y, yq, ysf);
     }
   } else {
     for (int v = tid; v < nvec; v += step) {
       float f[VN];
       const uint4 zero = make_uint4(0, 0, 0, 0);
-      if (live) take(xv[v], kRes ? rv[v] : zero, v, f);
+      take(xv[v], kRes ? rv[v] : zero, v, f);
     }
-    ss = row_sum(ss, red + 32 * threadIdx.y);
+    ss = row_sum(ss, red);
     const float inv = 1.0f / sqrtf(ss / (float)d + eps);
-    if (live && tid == 0 && inv_out) inv_out[row] = inv;
+    if (tid == 0 && inv_out) inv_out[row] = inv;
     const uint4* again = kRes ? sv : xv;
     for (int v0 = 0; v0 < nvec; v0 += step) {
       const int v = v0 + tid;
-      const bool active = live && v < nvec;
+      const bool active = v < nvec;
       uint4 a = make_uint4(0, 0, 0, 0), wr = a;
       if (active) {
         a = again[v];

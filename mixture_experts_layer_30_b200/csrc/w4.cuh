@@ -288,6 +288,7 @@ struct W4Problem {
 template <int GPS, int WR, int NT>
 struct W4Cfg {
   static_assert(WR >= NT, "a warp copies pieces of one column tile");
+  static_assert(WR < kW4Warps, "the warps of a pair join slices");
   static constexpr int kWk = kW4Warps / WR, kRows = 8 * NT;
   static constexpr int kDepth = 3;
   static constexpr int kScaleBytes = 2 * kW4Rows * GPS * 2;     // of a warp's two row blocks
@@ -610,41 +611,36 @@ struct W4Kernel {
         if (2 * u + 1 < rb_n) w4_store(p, it.r0, it.rows, 2 * u + 1, n, v1);
       }
     };
-    if constexpr (WK == 1) {
+    // slices 1.. leave their sums to slice 0, which adds them in slice order
+    auto pair_sync = [&] {
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + WK + wu), "n"(WK * 32) : "memory");
+    };
+    pair_sync();  // the last item's sums have been read
+    if (ks > 0) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) store(n, w4_scaled(acc[0][n]), w4_scaled(acc[1][n]));
-    } else {
-      // slices 1.. leave their sums to slice 0, which adds them in slice order
-      auto pair_sync = [&] {
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + WK + wu), "n"(WK * 32) : "memory");
-      };
-      pair_sync();  // the last item's sums have been read
-      if (ks > 0) {
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int n = 0; n < NT; ++n)
+          red[(((ks - 1) * 2 + m) * NT + n) * 32 + lane] = w4_scaled(acc[m][n]);
+    }
+    pair_sync();
+    if (ks == 0) {
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-            red[(((ks - 1) * 2 + m) * NT + n) * 32 + lane] = w4_scaled(acc[m][n]);
-      }
-      pair_sync();
-      if (ks == 0) {
+      for (int n = 0; n < NT; ++n) {
+        float4 v[2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float4 v[2];
+        for (int m = 0; m < 2; ++m) {
+          v[m] = w4_scaled(acc[m][n]);
 #pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            v[m] = w4_scaled(acc[m][n]);
-#pragma unroll
-            for (int k = 0; k < WK - 1; ++k) {
-              const float4 w = red[((k * 2 + m) * NT + n) * 32 + lane];
-              v[m].x += w.x;
-              v[m].y += w.y;
-              v[m].z += w.z;
-              v[m].w += w.w;
-            }
+          for (int k = 0; k < WK - 1; ++k) {
+            const float4 w = red[((k * 2 + m) * NT + n) * 32 + lane];
+            v[m].x += w.x;
+            v[m].y += w.y;
+            v[m].z += w.z;
+            v[m].w += w.w;
           }
-          store(n, v[0], v[1]);
         }
+        store(n, v[0], v[1]);
       }
     }
   }
