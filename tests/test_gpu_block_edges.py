@@ -3,7 +3,7 @@ import pytest
 import torch
 
 from mixture_experts_layer_30_b200 import binding as B
-from tests.test_gpu_w4 import offsets_of
+from tests.test_gpu_w4 import decode, offsets_of
 
 pytestmark = pytest.mark.gpu
 
@@ -231,3 +231,40 @@ def test_fp32_weight_gradient_keeps_small_rows(T):
     tol = want * 2.0 ** -24 + 32 * (per - 1) * 2.0 ** -25
     assert (T - 32) * 2.0 ** -25 > 2 * tol  # an fp32 join would be seen
     assert float((dw.double() - want).abs().max()) <= tol
+
+
+def test_w4_work_whose_cost_passes_32_bits():
+    """Runs are cut by cost * parts: in 64 bits where the product does not fit 32.  A contraction
+    of 8 and 65536 output columns reach that with small weights; every output is checked
+    (tolerance as for the other products: (K / 2 + 32) * 2^-23 of the sums' magnitude)."""
+    d, I, counts = 8, 65536, [25_003, 0, 15_006]
+    R = sum(counts)
+    ctas = 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    chunks = sum(c // 16 for c in counts)
+    assert chunks * 6 * (I // 64) * ctas >= 2 ** 32
+    g = torch.Generator().manual_seed(6)
+    shape = B.make_shape(R, d, 3, 0, 1, I, "bf16")
+    ws = B.new_workspace(shape)
+    W = [B.quantize_weights_w4(torch.randn((3, I, d), generator=g).to(torch.bfloat16).cuda(), 64)
+         for _ in range(2)]
+    x = torch.randn((R, d), generator=g).to(torch.bfloat16).cuda()
+    h = torch.full((R, I), float("nan"), dtype=torch.bfloat16, device="cuda")
+    off = offsets_of(counts)
+    B.expert_gate_up_w4(shape, 64, x, None, *W, off.cuda(), h, ws)
+    torch.cuda.synchronize()
+    assert B.device_status(ws) == 0
+    for e, m in enumerate(counts):
+        if m == 0:
+            continue
+        w1, w3 = (torch.from_numpy(decode((q[e:e + 1], s[e:e + 1]), I, d, 64)[0]).cuda()
+                  for q, s in W)
+        for a in range(int(off[e]), int(off[e + 1]), 1000):
+            b = min(a + 1000, int(off[e + 1]))
+            v = x[a:b].double()
+            p, u = v @ w1.T, v @ w3.T
+            act = p * torch.sigmoid(p)
+            want = act * u
+            mag = (1.1 * u.abs() * (v.abs() @ w1.abs().T) + act.abs() * (v.abs() @ w3.abs().T)
+                   + want.abs())
+            tol = (want.abs() * 2.0 ** -8 + mag * (d / 2 + 32) * 2.0 ** -23) * (1 + 2.0 ** -6)
+            assert ((h[a:b].double() - want).abs() <= tol + 1e-37).all(), (e, a)
