@@ -268,3 +268,44 @@ def test_w4_work_whose_cost_passes_32_bits():
                    + want.abs())
             tol = (want.abs() * 2.0 ** -8 + mag * (d / 2 + 32) * 2.0 ** -23) * (1 + 2.0 ** -6)
             assert ((h[a:b].double() - want).abs() <= tol + 1e-37).all(), (e, a)
+
+
+def test_short_tensors_on_the_device_are_refused():
+    """The native path of a call checks lengths too (nothing is launched)."""
+    T, d, N, Z, K, I = 16, 256, 4, 2, 2, 128
+    R = T * K
+    shape = B.make_shape(T, d, N, Z, K, I, "bf16")
+    ws = B.new_workspace(shape)
+    dev = dict(device="cuda")
+    u8, i32, bf = torch.uint8, torch.int32, torch.bfloat16
+    w1, w2 = (B.quantize_weights_w4(torch.zeros(s, dtype=bf, **dev), 64)
+              for s in ((N, I, d), (N, d, I)))
+    sizes = {"x_q": (T * d, u8), "x_sf": (T * d // 32, u8), "topk_idx": (R, i32),
+             "counts": (N + Z, i32), "offsets": (N + 1, i32), "row_token": (R, i32),
+             "slot_pos": (R, i32), "x_perm_q": (R * d, u8), "x_perm_sf": (R * d // 32, u8)}
+    before = B.kernel_launches()
+    for name in sizes:
+        a = [torch.zeros(n - (k == name), dtype=t, **dev) for k, (n, t) in sizes.items()]
+        with pytest.raises(ValueError, match=f"{name} has"):
+            B.permute_mxfp8_rows(shape, *a, ws)
+
+    def up(x=T * d, rows=R, off=N + 1, h=R * I):
+        B.expert_gate_up_w4(shape, 64, torch.zeros(x, dtype=bf, **dev),
+                            None if rows is None else torch.zeros(rows, dtype=i32, **dev), w1, w1,
+                            torch.zeros(off, dtype=i32, **dev), torch.zeros(h, dtype=bf, **dev), ws)
+
+    def down(h=R * I, off=N + 1, y=R * d):
+        B.expert_down_w4(shape, 64, torch.zeros(h, dtype=bf, **dev), w2,
+                         torch.zeros(off, dtype=i32, **dev), torch.zeros(y, dtype=bf, **dev), ws)
+    for call, args, name in ((up, dict(x=T * d - 1), "x"), (up, dict(rows=None), "x"),
+                             (up, dict(off=N), "offsets"), (up, dict(h=R * I - 1), "h"),
+                             (down, dict(h=R * I - 1), "h"), (down, dict(off=N), "offsets"),
+                             (down, dict(y=R * d - 1), "y_perm")):
+        with pytest.raises(ValueError, match=f"^{name} has"):
+            call(**args)
+    assert B.kernel_launches() == before
+    up()
+    up(x=R * d, rows=None)
+    down()
+    torch.cuda.synchronize()
+    assert B.device_status(ws) == 0
