@@ -173,8 +173,8 @@ template <typename T, int VPT, bool kSum>
 cudaError_t norm_bwd_launch(const NormBwdArgs& a, int threads, int groups, int* ctas) {
   auto* kernel = moe::rmsnorm_bwd_kernel<T, VPT, kSum>;
   const int smem = moe::bwd_depth(VPT) * (kSum ? 3 : 2) * VPT * threads * groups * 16;
-  // CTAs that an SM holds: by the ring, and by the 512 threads x 128 registers that the
-  // kernel may take
+  // CTAs an SM: what the ring leaves room for, 1024 threads and four CTAs at most.  Registers
+  // may let fewer reside at once; a CTA takes every *ctas-th group of rows either way.
   const int fit = smem ? (224 * 1024) / (smem + 2048) : 4;
   const int per_sm = std::max(1, std::min({4, fit, 1024 / (threads * groups)}));
   *ctas = std::min((a.T + groups - 1) / groups, std::min(sm_count() * per_sm, kNormBwdCtas));

@@ -9,9 +9,9 @@
 // memory time), so the sum over billions of elements keeps fp32 accuracy.  A vector
 // whose sum leaves fp32's range is summed again scaled by a power of two.  A CTA
 // sums its chunks in a fixed order and the last CTA to finish adds the CTAs'
-// sums in a fixed order: the norm is bit-reproducible.  403 M bf16 elements: 128 us
-// for the norm and 250 for the clipping, 6.3 TB/s each; 1.5 M elements in 53 tensors:
-// 7.9 us for both.
+// sums in a fixed order: the norm is bit-reproducible.  403 M bf16 elements: 385 to 388 us
+// for norm and clipping, 6.3 TB/s; the norm alone 120, 124 where every element is 0 and 148
+// where every vector is summed again.  1.5 M elements in 53 tensors: 8.0 us for both in a graph.
 #pragma once
 
 #include "common.cuh"

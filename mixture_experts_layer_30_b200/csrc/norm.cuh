@@ -13,8 +13,8 @@
 //
 // Both passes are bound by memory: a row is read once, kept in registers over
 // the reduction, and written once.  8192 x 6144 bf16 with the residual and the
-// MXFP8 output: 69 us, 6.6 TB/s, what a copy reaches; 16 x 2048: 1.5 us.  Backward
-// of the same size with dsum: 76 us with its two launches, 5.5 TB/s in the first
+// MXFP8 output: 70 us, 6.5 TB/s, what a copy reaches; 16 x 2048: 1.5 us in a graph.  Backward
+// of the same size with dsum: 77 us a pass, 5.5 TB/s in the first of its two launches
 // (a CTA per row and a register per value, which left no room for the next row's
 // loads: 641 us).
 #pragma once

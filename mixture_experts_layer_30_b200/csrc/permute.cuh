@@ -11,8 +11,9 @@
 //                         the chunk routed to e (warp bitmaps + popcount)
 //   4. gather_kernel      one warp per token: x row copied to each of its rows.
 // The dispatch of 8-bit rows runs 1-3 of a batch of up to 8192 tokens as one kernel of
-// one cluster (perm_cluster_kernel).  A batch of one chunk (decode) runs 1-4 as one kernel (perm_gather_small_kernel),
-// or 1-3 as perm_small_kernel when no copy is asked for.
+// up to eight clusters, each of which builds the whole batch's tables and ranks its share
+// of the tokens (perm_cluster_kernel).  A batch of one chunk (decode) runs 1-4 as one
+// kernel (perm_gather_small_kernel), or 1-3 as perm_small_kernel when no copy is asked for.
 #pragma once
 
 #include "common.cuh"

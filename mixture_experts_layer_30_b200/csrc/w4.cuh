@@ -180,8 +180,9 @@ w4_simt_kernel(const T* __restrict__ A, const uint32_t* __restrict__ q0,
 // pass over the codes.  Bound by instruction issue: a step below takes 280 to 340
 // instructions a warp, 144 of them to decode, and four warps a scheduler reach 0.6 of
 // the issue rate.  Down product at d = 6144, I = 2048, N = 32, 13 tokens, groups of 32:
-// 44 us, 5.1 TB/s; gate/up of the mid layer (64 x 2048 x 1024) at 256 tokens, groups of
-// 64: 58 us, 2.5 TB/s.  The same products on tcgen05 (codes decoded into tensor memory,
+// 47 to 49 us, 4.4 to 4.5 TB/s by the codes, scales and rows of the 30 experts that have
+// any; gate/up of the mid layer (64 x 2048 x 1024) at 256 tokens, groups of 64: 59 us,
+// 1.9 TB/s (49 experts).  The same products on tcgen05 (codes decoded into tensor memory,
 // the groups' sums read back for their scales) took longer up to 24 rows an expert: 60
 // against 48 us at 16 rows; a half step's chain of store, barrier, products and sums is
 // longer than its decoding.
